@@ -42,10 +42,13 @@ typedef enum {
     DSPARK_CUDA_ERROR = 5,        /* a CUDA runtime/driver call failed            */
     DSPARK_TIMEOUT = 6,           /* device: a bounded wait ran out               */
     DSPARK_INVALID_TOKEN = 7,     /* device: a token id or length out of range    */
-    DSPARK_BAD_LAUNCH = 8         /* device: a kernel found itself launched in a
+    DSPARK_BAD_LAUNCH = 8,        /* device: a kernel found itself launched in a
                                      shape it cannot run in (e.g. a tool re-issued
                                      the launch without its thread-block cluster);
                                      it returned before touching memory          */
+    DSPARK_OUT_OF_PAGES = 9,      /* device: a verify length was cut because the
+                                     free pages or the block table ran out       */
+    DSPARK_INVALID_PAGE = 10      /* device: a page id or cache slot out of range */
 } dspark_status;
 
 /* Text for a status code (static storage). */
@@ -293,6 +296,112 @@ int dspark_sts_fit(const float *z, const int32_t *accepted, int N, int gamma, do
 int dspark_schedule_prefix_noalloc(const float *P, int B, int gamma, const double *Tstep_us,
                                    int32_t *L_out, int32_t *N_out, double *objective_out,
                                    dspark_stream_t stream);
+
+/*
+ * The target's verification pass: the ragged batch that schedule_prefix's lengths call for,
+ * over a paged key-value cache.  (No counterpart on the DSpark pages, which take the target
+ * model as given: these calls join dspark_schedule_prefix to dspark_verify_prefix on the
+ * device, without the host knowing a length.)
+ *
+ * A cache has num_pages pages of page_size tokens; per layer the keys and the values are
+ * arrays [num_pages, Hkv, page_size, D] bf16, and slot s is token s mod page_size of page
+ * s / page_size.  Request b's tokens stand, in order, in pages pages[b, 0], pages[b, 1], ...
+ */
+
+/*
+ * Batch layout: block tables and slot map from the requests' lengths.
+ *
+ *   context [B] int32   tokens of request b in the cache before this step; -1 marks an idle
+ *                       slot, which gets no rows and holds no pages afterwards
+ *   L [B] int32         request b sends L[b] + 1 tokens, 0 <= L[b] <= gamma: its anchor and
+ *                       L[b] drafts (dspark_schedule_prefix's lengths), or a prompt
+ *   pages [B, max_pages] int32, held [B] int32
+ *                       block table, of which the first held[b] entries are request b's;
+ *                       the others are left as they are
+ *   free_pages [num_pages] int32, free_count [1] int32
+ *                       stack of unused pages, its top at free_pages[free_count - 1]
+ * For every request, with need = ceil((context + L + 1) / page_size): pages held beyond
+ * `need` go back on the stack, in request order and ascending place, then the pages that
+ * requests miss are popped one by one, in request order.  All five arrays are updated in
+ * place, but for context, which changes only with
+ *   accepted [B] int32 or null: context[b] += min(accepted[b] + 1, rows[b]) comes first, with
+ *                       rows the output of the preceding call: the last step's tokens that
+ *                       stuck (accepted as dspark_verify_prefix wrote it; -1 adds none)
+ * Rows of request b: n_b = L[b] + 1, or fewer where the free pages or the block table ran
+ * out; then L[b] becomes max(n_b - 1, 0) (verification stays lossless with any lengths) and
+ * DSPARK_OUT_OF_PAGES is recorded.
+ *   rows [B], row_start [B + 1] int32   n_b, and its running sum from 0
+ * and for row r = row_start[b] + i, 0 <= i < n_b:
+ *   position [row_capacity] int32   context[b] + i
+ *   slot [row_capacity] int32       pages[b, position / page_size] page_size + position mod page_size
+ *   token [row_capacity] int32      i ? x[b, i - 1] : anchor[b]; null: not written, and
+ *                                   anchor [B] and x [B, gamma] are not read
+ * Entries behind the last row are left as they are.  A call repeated with the same lengths
+ * changes nothing.  Supported sizes: 1 <= B <= 4096, 0 <= gamma <= 2^20, 1 <= page_size <=
+ * 65536, B max_pages < 2^31, num_pages page_size < 2^31; row_capacity >= B (gamma + 1).  A
+ * length out of range records DSPARK_INVALID_TOKEN and is clamped; a page id out of range
+ * records DSPARK_INVALID_PAGE and gives slot -1.
+ */
+int dspark_verify_layout(int32_t *L, const int32_t *anchor, const int32_t *x,
+                         const int32_t *accepted, int32_t *context, int32_t *rows, int32_t *pages,
+                         int32_t *held, int32_t *free_pages, int32_t *free_count, int B, int gamma,
+                         int page_size, int max_pages, int num_pages, int row_capacity,
+                         int32_t *row_start, int32_t *position, int32_t *slot, int32_t *token,
+                         dspark_stream_t stream);
+
+/*
+ * Queries and keys normalised per head and rotated, keys and values stored in the cache.
+ *
+ * Row r < *n_rows of qkv holds Hq query, Hkv key and Hkv value heads of D channels.  For each
+ * query and key head v, in fp32 with one rounding at the end:
+ *   y = v / sqrt(mean(v^2) + eps) * weight      (q_weight, k_weight; null: y = v)
+ *   (y_a, y_b) -> rope_scale (y_a cos - y_b sin, y_a sin + y_b cos)
+ * for the pairs (a, b) = (j, j + rot_dim / 2), or (2 j, 2 j + 1) with interleaved = 1,
+ * j < rot_dim / 2, at the angle position[r] inv_freq[j] (formed and reduced in fp64);
+ * channels from rot_dim on are not rotated.  Scaled rotary embeddings are a matter of the
+ * caller's inv_freq (fp32) and rope_scale.
+ *   qkv [row_capacity, qkv_stride] bf16, qkv_stride >= (Hq + 2 Hkv) D
+ *   n_rows [1] int32 (row_start + B of dspark_verify_layout)
+ *   q_out [row_capacity, Hq, D] bf16; rows from n_rows on are left as they are
+ *   k_cache, v_cache [num_pages, Hkv, page_size, D] bf16, written at slot[r]; none may
+ *   overlap qkv.  A slot outside [0, num_pages page_size) records DSPARK_INVALID_PAGE and
+ *   its key and value are not stored.  Slots of a call must differ from one another.
+ * Supported: D 64 or 128; rot_dim a multiple of 16 in [0, D]; qkv_stride % 8 == 0;
+ * Hq, Hkv <= 1024; num_pages page_size < 2^31; bf16 arrays 16-byte aligned.
+ */
+int dspark_qk_norm_rope_store(const void *qkv, int64_t qkv_stride, const void *q_weight,
+                              const void *k_weight, float eps, const float *inv_freq, int rot_dim,
+                              int interleaved, float rope_scale, const int32_t *position,
+                              const int32_t *slot, const int32_t *n_rows, int row_capacity, int Hq,
+                              int Hkv, int D, int page_size, int num_pages, void *q_out,
+                              void *k_cache, void *v_cache, dspark_stream_t stream);
+
+/*
+ * Attention of the batch's rows over the paged cache.
+ *
+ * Row r = row_start[b] + i stands at position context[b] + i and sees its request's keys
+ * 0 .. context[b] + i (its own among them: store them first), g = Hq / Hkv query heads to a
+ * key head:
+ *   out[r, h] = sum_j p_j v[j, h / g],  p = softmax_j(scale q[r, h] . k[j, h / g])
+ * fp32 scores, sums and accumulators.  Keys that a row does not see take no part, whatever
+ * their slots hold, NaN and infinities included.
+ *   q, out [row_capacity, Hq, D] bf16; rows behind the last request's are left as they are
+ *   pages [B, max_pages], context [B], row_start [B + 1] int32 as dspark_verify_layout leaves
+ *   them (context: -1 or any other value where a request has no rows)
+ *   workspace, workspace_bytes >= dspark_verify_attention_workspace_bytes(Hq, Hkv, D);
+ *   256-byte aligned, no initialisation needed.  Calls that can overlap need one each.
+ * A page id out of range records DSPARK_INVALID_PAGE and is read as page 0; lengths beyond
+ * the block table record DSPARK_INVALID_TOKEN and are clamped.
+ * Supported: D 64 or 128; Hq a multiple of Hkv, Hq / Hkv <= 128; page_size 16, 32, 64 or
+ * 128; 1 <= B <= 4096; num_pages Hkv page_size < 2^31, B max_pages < 2^31; arrays 16-byte
+ * aligned; scale finite.
+ */
+size_t dspark_verify_attention_workspace_bytes(int Hq, int Hkv, int D);
+int dspark_verify_attention(const void *q, const void *k_cache, const void *v_cache,
+                            const int32_t *pages, const int32_t *context, const int32_t *row_start,
+                            int B, int row_capacity, int Hq, int Hkv, int D, int page_size,
+                            int max_pages, int num_pages, float scale, void *out, void *workspace,
+                            size_t workspace_bytes, dspark_stream_t stream);
 
 /* Synchronises `stream`, then reads and clears the device error word of the
  * current device into *status (DSPARK_OK when nothing was recorded). */

@@ -13,6 +13,12 @@ raises.
     schedule_prefix   hardware-aware prefix scheduler (global top-N + scan)
     verify_prefix     strict prefix-match verification
     sts_fit           fitting the per-position temperatures (ECE grid search)
+
+and, for the target's verification pass between the scheduler and the verification:
+
+    verify_layout       ragged batch over a paged cache: block tables, positions, slots
+    qk_norm_rope_store  query/key norm and rotary positions, keys and values to the cache
+    verify_attention    attention of the batch's rows over the paged cache
 """
 from __future__ import annotations
 
@@ -24,14 +30,15 @@ from . import _build
 __all__ = [
     "DSparkError", "load", "workspace_bytes", "draft_step", "draft_step_rnn",
     "draft_confidence_step", "step", "confidence_sts", "schedule_prefix",
-    "verify_prefix", "sts_fit_workspace_bytes", "sts_fit", "get_error", "status_string", "set_wait_timeout_ns", "debug_barrier_extra",
+    "verify_prefix", "verify_layout", "qk_norm_rope_store", "verify_attention_workspace_bytes",
+    "verify_attention", "sts_fit_workspace_bytes", "sts_fit", "get_error", "status_string", "set_wait_timeout_ns", "debug_barrier_extra",
     "STATUS",
 ]
 
 STATUS = {
     0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED_SHAPE", 3: "WORKSPACE_TOO_SMALL",
     4: "NOT_MONOTONE", 5: "CUDA_ERROR", 6: "TIMEOUT", 7: "INVALID_TOKEN",
-    8: "BAD_LAUNCH",
+    8: "BAD_LAUNCH", 9: "OUT_OF_PAGES", 10: "INVALID_PAGE",
 }
 
 EXPORTED = (
@@ -39,7 +46,9 @@ EXPORTED = (
     "dspark_confidence_sts", "dspark_schedule_prefix", "dspark_verify_prefix",
     "dspark_get_error", "dspark_set_wait_timeout_ns", "dspark_debug_barrier_extra",
     "dspark_sts_fit_workspace_bytes", "dspark_sts_fit", "dspark_draft_step_rnn",
-    "dspark_draft_confidence_step", "dspark_step",
+    "dspark_draft_confidence_step", "dspark_step", "dspark_verify_layout",
+    "dspark_qk_norm_rope_store", "dspark_verify_attention_workspace_bytes",
+    "dspark_verify_attention",
 )
 
 _lib = None
@@ -76,6 +85,12 @@ def load(build_if_missing: bool = True):
                                 p, p, p, p, p, p, p, p, p, p, sz, p]
     lib.dspark_schedule_prefix.argtypes = [p, i, i, p, p, p, p, p, sz, p]
     lib.dspark_verify_prefix.argtypes = [p, p, p, i, i, p, p, p]
+    lib.dspark_verify_layout.argtypes = [p] * 10 + [i] * 6 + [p] * 5
+    lib.dspark_qk_norm_rope_store.argtypes = [p, C.c_int64, p, p, f32, p, i, i, f32, p, p, p, i, i,
+                                              i, i, i, i, p, p, p, p]
+    lib.dspark_verify_attention_workspace_bytes.argtypes = [i, i, i]
+    lib.dspark_verify_attention_workspace_bytes.restype = sz
+    lib.dspark_verify_attention.argtypes = [p] * 6 + [i] * 8 + [f32, p, p, sz, p]
     lib.dspark_sts_fit_workspace_bytes.argtypes = [i, i, i, i]
     lib.dspark_sts_fit_workspace_bytes.restype = sz
     lib.dspark_sts_fit.argtypes = [p, p, i, i, C.c_double, C.c_double, i, i, p, p, p, p, sz, p]
@@ -84,6 +99,7 @@ def load(build_if_missing: bool = True):
     lib.dspark_debug_barrier_extra.argtypes = [i]
     for name in EXPORTED:
         if name not in ("dspark_status_string", "dspark_workspace_bytes",
+                        "dspark_verify_attention_workspace_bytes",
                         "dspark_sts_fit_workspace_bytes"):
             getattr(lib, name).restype = i
     _lib = lib
@@ -230,6 +246,134 @@ def verify_prefix(x, L, target, accepted_out, bonus_out, stream=None):
         B, gamma, _dev(accepted_out, torch.int32, "accepted_out"),
         _dev(bonus_out, torch.int32, "bonus_out"), _stream(stream))
     _check("dspark_verify_prefix", st)
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _one_device(**tensors):
+    """The library launches on the current device: every tensor must be there."""
+    import torch
+    here = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda and t.device.index != here:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+
+
+def verify_layout(L, context, rows, pages, held, free_pages, free_count, row_start, position, slot,
+                  page_size: int, gamma: int, anchor=None, x=None, token=None, accepted=None,
+                  stream=None):
+    """Lay a verification step's ragged batch over a paged cache (see dspark_verify_layout).
+
+    L, context, rows, held, accepted [B]; pages [B, max_pages]; free_pages [num_pages];
+    free_count [1]; row_start [B + 1]; position, slot, token [row_capacity]; anchor [B],
+    x [B, gamma]: all int32.  L, context, rows, pages, held, free_pages and free_count are
+    the cache's state, updated in place."""
+    import torch
+    i32 = torch.int32
+    B, max_pages = pages.shape
+    cap = position.numel()
+    if (anchor is None) != (token is None) or (x is None) != (token is None):
+        raise ValueError("anchor, x and token go together")
+    args = dict(L=L, anchor=anchor, x=x, accepted=accepted, context=context, rows=rows, pages=pages,
+                held=held, free_pages=free_pages, free_count=free_count, row_start=row_start,
+                position=position, slot=slot, token=token)
+    ptr = {k: None if t is None else _dev(t, i32, k) for k, t in args.items()}
+    _one_device(**args)
+    for name in ("L", "context", "rows", "held", "anchor", "accepted"):
+        if args[name] is not None:
+            _shape(args[name], (B,), name)
+    _shape(row_start, (B + 1,), "row_start")
+    _shape(free_count, (1,), "free_count")
+    for name in ("position", "slot", "token"):
+        if args[name] is not None:
+            _shape(args[name], (cap,), name)
+    if x is not None:
+        _shape(x, (B, gamma), "x")
+    st = load().dspark_verify_layout(
+        ptr["L"], ptr["anchor"], ptr["x"], ptr["accepted"], ptr["context"], ptr["rows"],
+        ptr["pages"], ptr["held"], ptr["free_pages"], ptr["free_count"], B, int(gamma),
+        int(page_size), max_pages, free_pages.numel(), cap, ptr["row_start"], ptr["position"],
+        ptr["slot"], ptr["token"], _stream(stream))
+    _check("dspark_verify_layout", st)
+
+
+def qk_norm_rope_store(qkv, position, slot, n_rows, q_out, k_cache, v_cache, q_weight=None,
+                       k_weight=None, eps: float = 1e-6, inv_freq=None, interleaved: bool = False,
+                       rope_scale: float = 1.0, stream=None):
+    """Normalise and rotate queries and keys, store keys and values in the paged cache (see
+    dspark_qk_norm_rope_store).
+
+    qkv [row_capacity, (Hq + 2 Hkv) D] bf16, rows may be strided; position, slot
+    [row_capacity] int32; n_rows [1] int32; q_out [row_capacity, Hq, D]; caches [num_pages,
+    Hkv, page_size, D]; weights [D] bf16; inv_freq [rot_dim / 2] fp32."""
+    import torch
+    bf = torch.bfloat16
+    cap, Hq, D = q_out.shape
+    num_pages, Hkv, page_size, _ = k_cache.shape
+    if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda or qkv.dtype != bf:
+        raise TypeError("qkv must be a CUDA tensor of torch.bfloat16")
+    _shape(qkv, (cap, (Hq + 2 * Hkv) * D), "qkv")
+    if qkv.stride(1) != 1:
+        raise ValueError("qkv must be contiguous along its channels")
+    stride = qkv.stride(0) if cap > 1 else qkv.shape[1]
+    _shape(k_cache, (num_pages, Hkv, page_size, D), "k_cache")
+    _shape(v_cache, k_cache.shape, "v_cache")
+    _shape(position, (cap,), "position")
+    _shape(slot, (cap,), "slot")
+    _shape(n_rows, (1,), "n_rows")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _shape(w, (D,), name)
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise ValueError("inv_freq must have one dimension")
+    _one_device(qkv=qkv, position=position, slot=slot, n_rows=n_rows, q_out=q_out, k_cache=k_cache,
+                v_cache=v_cache, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq)
+    st = load().dspark_qk_norm_rope_store(
+        C.c_void_p(qkv.data_ptr()), stride,
+        None if q_weight is None else _dev(q_weight, bf, "q_weight"),
+        None if k_weight is None else _dev(k_weight, bf, "k_weight"), float(eps),
+        None if inv_freq is None else _dev(inv_freq, torch.float32, "inv_freq"),
+        0 if inv_freq is None else 2 * inv_freq.numel(), int(bool(interleaved)), float(rope_scale),
+        _dev(position, torch.int32, "position"), _dev(slot, torch.int32, "slot"),
+        _dev(n_rows, torch.int32, "n_rows"), cap, Hq, Hkv, D, page_size, num_pages,
+        _dev(q_out, bf, "q_out"), _dev(k_cache, bf, "k_cache"), _dev(v_cache, bf, "v_cache"),
+        _stream(stream))
+    _check("dspark_qk_norm_rope_store", st)
+
+
+def verify_attention_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
+    return int(load().dspark_verify_attention_workspace_bytes(Hq, Hkv, D))
+
+
+def verify_attention(q, k_cache, v_cache, pages, context, row_start, out, workspace, scale=None,
+                     stream=None):
+    """Attention of a verification batch's rows over the paged cache (see
+    dspark_verify_attention).
+
+    q, out [row_capacity, Hq, D]; caches [num_pages, Hkv, page_size, D] bf16; pages
+    [B, max_pages], context [B], row_start [B + 1] int32.  scale defaults to D ** -0.5."""
+    import torch
+    bf, i32 = torch.bfloat16, torch.int32
+    cap, Hq, D = q.shape
+    num_pages, Hkv, page_size, _ = k_cache.shape
+    B, max_pages = pages.shape
+    _shape(k_cache, (num_pages, Hkv, page_size, D), "k_cache")
+    _shape(v_cache, k_cache.shape, "v_cache")
+    _shape(context, (B,), "context")
+    _shape(row_start, (B + 1,), "row_start")
+    _shape(out, q.shape, "out")
+    _one_device(q=q, k_cache=k_cache, v_cache=v_cache, pages=pages, context=context,
+                row_start=row_start, out=out, workspace=workspace)
+    st = load().dspark_verify_attention(
+        _dev(q, bf, "q"), _dev(k_cache, bf, "k_cache"), _dev(v_cache, bf, "v_cache"),
+        _dev(pages, i32, "pages"), _dev(context, i32, "context"),
+        _dev(row_start, i32, "row_start"), B, cap, Hq, Hkv, D, page_size, max_pages, num_pages,
+        float(D ** -0.5 if scale is None else scale), _dev(out, bf, "out"),
+        _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream))
+    _check("dspark_verify_attention", st)
 
 
 def sts_fit_workspace_bytes(N: int, gamma: int, n_t: int, n_bins: int) -> int:

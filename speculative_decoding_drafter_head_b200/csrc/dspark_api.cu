@@ -1,10 +1,11 @@
 // dspark_api.cu -- the C ABI (include/dspark.h): argument checks, TMA descriptors and
-// launches of the four hot-path kernels.  One translation unit holds every kernel so
+// launches of the kernels.  One translation unit holds every kernel so
 // that the per-device error word is a single symbol.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -14,8 +15,11 @@
 #include "markov_draft.cuh"
 #include "markov_pair.cuh"
 #include "ptx.cuh"
+#include "qk_norm_rope.cuh"
 #include "schedule_prefix.cuh"
 #include "sts_fit.cuh"
+#include "verify_attention.cuh"
+#include "verify_layout.cuh"
 #include "verify_prefix.cuh"
 
 namespace {
@@ -162,6 +166,8 @@ const char *dspark_status_string(int status)
     case DSPARK_TIMEOUT: return "device wait timed out";
     case DSPARK_INVALID_TOKEN: return "token id or verify length out of range";
     case DSPARK_BAD_LAUNCH: return "kernel launched in a shape it cannot run in";
+    case DSPARK_OUT_OF_PAGES: return "verify length cut: free pages or block table ran out";
+    case DSPARK_INVALID_PAGE: return "page id or cache slot out of range";
     default: return "unknown status";
     }
 }
@@ -639,6 +645,187 @@ int dspark_verify_prefix(const int32_t *x, const int32_t *L, const int32_t *targ
     if (int st = current_device(&dev)) return st;
     Vf::verify_prefix_kernel<<<(B + Vf::kThreads - 1) / Vf::kThreads, Vf::kThreads, 0, stream>>>(
         x, L, target, B, gamma, accepted_out, bonus_out);
+    return from_cuda(cudaGetLastError());
+}
+
+int dspark_verify_layout(int32_t *L, const int32_t *anchor, const int32_t *x,
+                         const int32_t *accepted, int32_t *context, int32_t *rows, int32_t *pages,
+                         int32_t *held, int32_t *free_pages, int32_t *free_count, int B, int gamma,
+                         int page_size, int max_pages, int num_pages, int row_capacity,
+                         int32_t *row_start, int32_t *position, int32_t *slot, int32_t *token,
+                         dspark_stream_t stream)
+{
+    namespace Y = dspark::layout;
+    if (!L || !context || !rows || !pages || !held || !free_pages || !free_count || !row_start ||
+        !position || !slot)
+        return DSPARK_INVALID_ARG;
+    if (token && (!anchor || (!x && gamma > 0))) return DSPARK_INVALID_ARG;
+    for (const void *a : {static_cast<const void *>(L), static_cast<const void *>(anchor),
+                          static_cast<const void *>(x), static_cast<const void *>(accepted),
+                          static_cast<const void *>(context), static_cast<const void *>(rows),
+                          static_cast<const void *>(pages), static_cast<const void *>(held),
+                          static_cast<const void *>(free_pages),
+                          static_cast<const void *>(free_count),
+                          static_cast<const void *>(row_start), static_cast<const void *>(position),
+                          static_cast<const void *>(slot), static_cast<const void *>(token)})
+        if (!aligned(a, 4)) return DSPARK_INVALID_ARG;
+    if (B < 1 || B > Y::kMaxB || gamma < 0 || gamma > (1 << 20) || page_size < 1 ||
+        page_size > 65536 || max_pages < 1 || num_pages < 1 ||
+        static_cast<long long>(B) * max_pages > INT32_MAX ||
+        static_cast<long long>(num_pages) * page_size > INT32_MAX)
+        return DSPARK_UNSUPPORTED_SHAPE;
+    if (row_capacity < static_cast<long long>(B) * (gamma + 1)) return DSPARK_INVALID_ARG;
+    DeviceInfo *dev = nullptr;
+    if (int st = current_device(&dev)) return st;
+    Y::Params prm;
+    prm.L = L;
+    prm.anchor = anchor;
+    prm.x = x;
+    prm.accepted = accepted;
+    prm.context = context;
+    prm.rows = rows;
+    prm.pages = pages;
+    prm.held = held;
+    prm.free_pages = free_pages;
+    prm.free_count = free_count;
+    prm.B = B;
+    prm.gamma = gamma;
+    prm.ps = page_size;
+    prm.max_pages = max_pages;
+    prm.num_pages = num_pages;
+    prm.row_start = row_start;
+    prm.position = position;
+    prm.slot = slot;
+    prm.token = token;
+    const size_t smem = static_cast<size_t>(B) * Y::kWordsPerRequest * 4;
+    if (smem > 40 * 1024 &&
+        cudaFuncSetAttribute(Y::verify_layout_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Y::kMaxB * Y::kWordsPerRequest * 4) != cudaSuccess)
+        return DSPARK_CUDA_ERROR;
+    // one CTA for the rows of up to one thread each, then more, up to a portable cluster
+    const long long most = static_cast<long long>(B) * (gamma + 1);
+    int ctas = 1;
+    while (ctas < 8 && most > static_cast<long long>(ctas) * Y::kThreads) ctas *= 2;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(Y::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return from_cuda(cudaLaunchKernelEx(&cfg, Y::verify_layout_kernel, prm));
+}
+
+int dspark_qk_norm_rope_store(const void *qkv, int64_t qkv_stride, const void *q_weight,
+                              const void *k_weight, float eps, const float *inv_freq, int rot_dim,
+                              int interleaved, float rope_scale, const int32_t *position,
+                              const int32_t *slot, const int32_t *n_rows, int row_capacity, int Hq,
+                              int Hkv, int D, int page_size, int num_pages, void *q_out,
+                              void *k_cache, void *v_cache, dspark_stream_t stream)
+{
+    namespace Q = dspark::qknorm;
+    if (!qkv || !position || !slot || !n_rows || !q_out || !k_cache || !v_cache)
+        return DSPARK_INVALID_ARG;
+    if (!aligned(qkv, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) ||
+        !aligned(q_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(inv_freq, 4) || !aligned(position, 4) || !aligned(slot, 4) || !aligned(n_rows, 4))
+        return DSPARK_INVALID_ARG;
+    if (!(eps >= 0.0f) || !std::isfinite(eps) || !std::isfinite(rope_scale) ||
+        (interleaved != 0 && interleaved != 1) || (rot_dim > 0 && !inv_freq))
+        return DSPARK_INVALID_ARG;
+    if ((D != 64 && D != 128) || rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0 || Hq < 1 ||
+        Hq > 1024 || Hkv < 1 || Hkv > 1024 || row_capacity < 1 || page_size < 1 || num_pages < 1 ||
+        static_cast<long long>(num_pages) * page_size > INT32_MAX || qkv_stride % 8 != 0)
+        return DSPARK_UNSUPPORTED_SHAPE;
+    if (qkv_stride < static_cast<int64_t>(Hq + 2 * Hkv) * D) return DSPARK_INVALID_ARG;
+    DeviceInfo *dev = nullptr;
+    if (int st = current_device(&dev)) return st;
+    Q::Params prm;
+    prm.qkv = static_cast<const uint16_t *>(qkv);
+    prm.stride = qkv_stride;
+    prm.q_weight = static_cast<const uint16_t *>(q_weight);
+    prm.k_weight = static_cast<const uint16_t *>(k_weight);
+    prm.eps = eps;
+    prm.inv_freq = inv_freq;
+    prm.rot = rot_dim;
+    prm.interleaved = interleaved;
+    prm.rope_scale = rope_scale;
+    prm.position = position;
+    prm.slot = slot;
+    prm.n_rows = n_rows;
+    prm.row_capacity = row_capacity;
+    // one row to a CTA while the rows leave SMs idle
+    prm.tile = row_capacity <= 8 * dev->sms ? 1 : Q::kMaxTile;
+    prm.Hq = Hq;
+    prm.Hkv = Hkv;
+    prm.ps = page_size;
+    prm.num_pages = num_pages;
+    prm.q_out = static_cast<uint16_t *>(q_out);
+    prm.k_cache = static_cast<uint16_t *>(k_cache);
+    prm.v_cache = static_cast<uint16_t *>(v_cache);
+    const int grid = (row_capacity - 1) / prm.tile + 1;
+    if (D == 64)
+        Q::qk_norm_rope_store_kernel<64><<<grid, Q::kThreads, 0, stream>>>(prm);
+    else
+        Q::qk_norm_rope_store_kernel<128><<<grid, Q::kThreads, 0, stream>>>(prm);
+    return from_cuda(cudaGetLastError());
+}
+
+size_t dspark_verify_attention_workspace_bytes(int Hq, int Hkv, int D)
+{
+    if (Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
+    return 256;
+}
+
+int dspark_verify_attention(const void *q, const void *k_cache, const void *v_cache,
+                            const int32_t *pages, const int32_t *context, const int32_t *row_start,
+                            int B, int row_capacity, int Hq, int Hkv, int D, int page_size,
+                            int max_pages, int num_pages, float scale, void *out, void *workspace,
+                            size_t workspace_bytes, dspark_stream_t stream)
+{
+    namespace A = dspark::vattn;
+    if (!q || !k_cache || !v_cache || !pages || !context || !row_start || !out || !workspace)
+        return DSPARK_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(pages, 4) || !aligned(context, 4) || !aligned(row_start, 4) ||
+        !aligned(workspace, 256) || !std::isfinite(scale))
+        return DSPARK_INVALID_ARG;
+    if ((D != 64 && D != 128) || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 128 ||
+        (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) || B < 1 ||
+        B > A::kMaxB || row_capacity < 1 || max_pages < 1 || num_pages < 1 ||
+        static_cast<long long>(B) * max_pages > INT32_MAX ||
+        static_cast<long long>(num_pages) * page_size > INT32_MAX / Hkv)
+        return DSPARK_UNSUPPORTED_SHAPE;
+    if (workspace_bytes < dspark_verify_attention_workspace_bytes(Hq, Hkv, D))
+        return DSPARK_WORKSPACE_TOO_SMALL;
+    DeviceInfo *dev = nullptr;
+    if (int st = current_device(&dev)) return st;
+    A::Params prm;
+    prm.q = static_cast<const uint16_t *>(q);
+    prm.k_cache = static_cast<const uint16_t *>(k_cache);
+    prm.v_cache = static_cast<const uint16_t *>(v_cache);
+    prm.pages = pages;
+    prm.context = context;
+    prm.row_start = row_start;
+    prm.B = B;
+    prm.row_capacity = row_capacity;
+    prm.Hq = Hq;
+    prm.Hkv = Hkv;
+    prm.ps = page_size;
+    prm.max_pages = max_pages;
+    prm.num_pages = num_pages;
+    prm.scale = scale;
+    prm.out = static_cast<uint16_t *>(out);
+    if (D == 64)
+        A::verify_attention_kernel<64><<<dim3(row_capacity, Hq), A::kThreads, 0, stream>>>(prm);
+    else
+        A::verify_attention_kernel<128><<<dim3(row_capacity, Hq), A::kThreads, 0, stream>>>(prm);
     return from_cuda(cudaGetLastError());
 }
 
