@@ -780,7 +780,7 @@ int dspark_qk_norm_rope_store(const void *qkv, int64_t qkv_stride, const void *q
 size_t dspark_verify_attention_workspace_bytes(int Hq, int Hkv, int D)
 {
     if (Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
-    return 256;
+    return dspark::vattn::workspace_layout(D).total;
 }
 
 int dspark_verify_attention(const void *q, const void *k_cache, const void *v_cache,
@@ -806,6 +806,25 @@ int dspark_verify_attention(const void *q, const void *k_cache, const void *v_ca
         return DSPARK_WORKSPACE_TOO_SMALL;
     DeviceInfo *dev = nullptr;
     if (int st = current_device(&dev)) return st;
+    EncodeTiledFn encode = encode_tiled();
+    if (!encode) return DSPARK_CUDA_ERROR;
+    // one box: 64 channels of a page's tokens of one head
+    CUtensorMap tm_k, tm_v;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D),
+                                static_cast<cuuint64_t>(num_pages) * Hkv * page_size};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(page_size)};
+    const cuuint32_t estr[2] = {1, 1};
+    for (int kv = 0; kv < 2; ++kv)
+        if (encode(kv ? &tm_v : &tm_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                   const_cast<void *>(kv ? v_cache : k_cache), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return DSPARK_CUDA_ERROR;
+
+    const A::Layout lay = A::workspace_layout(D);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     A::Params prm;
     prm.q = static_cast<const uint16_t *>(q);
     prm.k_cache = static_cast<const uint16_t *>(k_cache);
@@ -817,16 +836,42 @@ int dspark_verify_attention(const void *q, const void *k_cache, const void *v_ca
     prm.row_capacity = row_capacity;
     prm.Hq = Hq;
     prm.Hkv = Hkv;
+    prm.group = Hq / Hkv;
     prm.ps = page_size;
     prm.max_pages = max_pages;
     prm.num_pages = num_pages;
-    prm.scale = scale;
+    prm.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
     prm.out = static_cast<uint16_t *>(out);
-    if (D == 64)
-        A::verify_attention_kernel<64><<<dim3(row_capacity, Hq), A::kThreads, 0, stream>>>(prm);
-    else
-        A::verify_attention_kernel<128><<<dim3(row_capacity, Hq), A::kThreads, 0, stream>>>(prm);
-    return from_cuda(cudaGetLastError());
+    prm.desc = reinterpret_cast<int4 *>(ws);
+    prm.part_ml = reinterpret_cast<float2 *>(ws + lay.ml);
+    prm.part_o = reinterpret_cast<float *>(ws + lay.o);
+    prm.timeout_ns = g_timeout_ns.load();
+    // query tiles of 64 rows where a request's share of the row capacity (its gamma + 1 tokens,
+    // when the batch layout made it) fits one, else of 128
+    const bool wide = static_cast<long long>((row_capacity - 1) / B + 1) * prm.group > 64;
+    prm.tokens = (wide ? 128 : 64) / prm.group;
+    void (*kern)(const CUtensorMap, const CUtensorMap, const A::Params) =
+        D == 64 ? (wide ? A::verify_attention_kernel<64, 128> : A::verify_attention_kernel<64, 64>)
+                : (wide ? A::verify_attention_kernel<128, 128> : A::verify_attention_kernel<128, 64>);
+    const int smem = D == 64 ? (wide ? A::smem_bytes<64, 128>() : A::smem_bytes<64, 64>())
+                             : (wide ? A::smem_bytes<128, 128>() : A::smem_bytes<128, 64>());
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return DSPARK_CUDA_ERROR;
+    const int grid = dev->sms < A::kMaxCtas ? dev->sms : A::kMaxCtas;
+    kern<<<grid, A::kThreads, smem, stream>>>(tm_k, tm_v, prm);
+    if (cudaGetLastError() != cudaSuccess) return DSPARK_CUDA_ERROR;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(grid, A::kJoinSplit);
+    cfg.blockDim = dim3(A::kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return from_cuda(cudaLaunchKernelEx(
+        &cfg, D == 64 ? A::verify_join_kernel<64> : A::verify_join_kernel<128>, prm));
 }
 
 size_t dspark_sts_fit_workspace_bytes(int N, int gamma, int n_t, int n_bins)

@@ -4,100 +4,917 @@
 //     out[r, h] = sum_j softmax_j(scale q[r, h] . k[j, h / g]) v[j, h / g]
 // with j running over the request's block table and g = Hq / Hkv query heads to a key head.
 //
-// One CTA per (row, query head): each thread scores one key of a tile of 128, the softmax's
-// maximum and sum run along the tiles (fp32), and each thread then adds up one channel.
+// What bounds it: HBM.  The cache is read once, 4 D bytes for a key and its value, and serves
+// the n = (L + 1) g rows that share a key head (17 x 4 at most at the benchmark's shapes): n
+// flops a byte, far below the tensor cores' 250.  So the keys, not the rows, fill the 128
+// lanes of an MMA, and no lane is padding whatever n is:
+//     S^T [128 keys x n] = K Q^T         A = K tile (K-major), B = Q (K-major)
+//     O^T [D x n] += V^T P               A = V tile (M-major), B = P [keys x n] (N-major)
+//     l [n]       += 1^T P               A = ones (64 x 16), the softmax's sum
+// n is rounded up to 16 for each unit of work.  The sum comes from the tensor core for the
+// price of A's rows, in fp32, of the same rounded weights as O; no thread adds up anything.
+//
+// Softmax: a thread owns one key and all n rows.  exp2 needs a reference m per row that keeps
+// the weights in range, not the maximum itself: m is the maximum over the unit's first key
+// tile, and stays until some score exceeds it by more than 2^24 in weight; then m rises to the
+// new maximum and O and l are scaled (one vote a tile, folded into the barrier that a tile
+// needs anyway).  bf16 weights keep their 8 bits at any magnitude, and O and l are fp32, so
+// a stale m costs no accuracy.  Rounding the weights to bf16 (2^-9 of each, twice under the
+// output's own rounding) is what the tensor core's second product asks for.
+//
+// Masks: key j is seen by the rows from (j - context) g on, so a thread compares the row's
+// number with one number of its own.  Values behind the last key are cleared in shared memory
+// (0 x NaN is NaN); values of the step's own rows that are not finite are cleared as well and
+// added at the end to the rows that see them, so that they reach no row that does not.
+//
+// Work: key tiles in one line, an equal share for each of 148 CTAs (verify_plan.h), because
+// lengths are known to the device alone and differ by orders of magnitude.  Units cut by a
+// border leave (m, l, O) in the workspace, and verify_join_kernel adds the parts up, in
+// order, so results do not depend on timing.  It is launched to overlap with this kernel's end.
+//
+// Warps: 0-3 softmax and output (thread = key of the tile, then channel of the output), 4
+// copies K and V pages into a ring of 32 KB tiles by TMA (one box a page), 5 issues the MMAs,
+// 6 and 7 copy Q.  S and P are double-buffered, so S of the next tile and O of the last run
+// beside the softmax; a unit's output is written after the next unit's first softmax.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "ptx.cuh"
+#include "verify_plan.h"
 
 namespace dspark {
 namespace vattn {
 
-constexpr int kThreads = 128;
+using vplan::kTileKeys;
+
 constexpr int kMaxB = 4096;
+constexpr int kMaxCtas = 160;                     // grid: one CTA per SM, at most this many
+constexpr int kMaxRows = 128;                     // rows of a query tile
+constexpr int kThreads = 256;
+constexpr int kSoftThreads = 128;
+constexpr int kWarpLoad = 4, kWarpMma = 5, kWarpQ = 6;
+constexpr int kQThreads = 64;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kWaitHintNs = 20000;
+constexpr float kRaise = 24.0f;                   // log2 of the weight at which m rises
+constexpr int kOnesBytes = 1152;                  // 8 x 2 core matrices of 128 B, one apart
+constexpr int kJoinThreads = 128;
+constexpr int kJoinSplit = 4;                     // CTAs that share a unit's rows
 
 struct Params {
     const uint16_t *q, *k_cache, *v_cache;
     const int32_t *pages, *context, *row_start;
-    int B, row_capacity, Hq, Hkv, ps, max_pages, num_pages;
-    float scale;
+    int B, row_capacity, Hq, Hkv, group, tokens, ps, max_pages, num_pages;
+    float scale_log2;                             // scale log2(e)
     uint16_t *out;
+    int4 *desc;                                   // [ctas] the unit that starts a join
+    float2 *part_ml;                              // [ctas][2][kMaxRows] (m, l)
+    float *part_o;                                // [ctas][2][kMaxRows][D]
+    unsigned long long timeout_ns;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) verify_attention_kernel(const Params p)
+// Workspace: descriptors, then (m, l), then O, two parts a CTA.
+struct Layout {
+    size_t ml, o, total;
+};
+__host__ __device__ inline Layout workspace_layout(int D)
 {
-    __shared__ float q_s[D], p_s[kThreads], red[4];
-    __shared__ const uint16_t *v_s[kThreads];
-    const int row = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-    if (row >= min(max(p.row_start[p.B], 0), p.row_capacity)) return;
-    int lo = 0, hi = p.B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.row_start[mid] <= row) lo = mid;
-        else hi = mid - 1;
+    Layout w;
+    w.ml = (kMaxCtas * sizeof(int4) + 255) / 256 * 256;
+    w.o = w.ml + static_cast<size_t>(kMaxCtas) * 2 * kMaxRows * sizeof(float2);
+    w.total = w.o + static_cast<size_t>(kMaxCtas) * 2 * kMaxRows * D * sizeof(float);
+    return w;
+}
+
+// kN: rows of a query tile at most.  Two Q buffers, two O and l accumulators and five ring
+// tiles fit beside 64 rows; 128 rows leave room for one of each and four tiles.
+template <int D, int kN>
+struct Cfg {
+    static constexpr int kQBufs = kN == 64 ? 2 : 1;
+    static constexpr int kOBufs = kN == 64 ? 2 : 1;
+    static constexpr int kPBufs = kN == 64 ? 2 : 1;
+    static constexpr int kTileBytes = kTileKeys * D * 2;
+    static constexpr int kHalfBytes = kTileKeys * 128;       // 64 channels of a tile
+    static constexpr int kStages = (kN == 64 ? 5 : 4) * (128 / D);
+    static constexpr int kQBytes = kN * D * 2;
+    static constexpr int kPBytes = kTileKeys * kN * 2;
+    static constexpr int kRing = 0;
+    static constexpr int kQ = kRing + kStages * kTileBytes;
+    static constexpr int kP = kQ + kQBufs * kQBytes;
+    static constexpr int kOnes = kP + kPBufs * kPBytes;
+    static constexpr int kM = kOnes + kOnesBytes;            // float [2][kN]
+    static constexpr int kRed = kM + 2 * kN * 4;             // float [4][kN]
+    static constexpr int kCtl = kRed + 4 * kN * 4;
+    static constexpr uint32_t kColS = 0, kColO = 2 * kN, kColL = kColO + kOBufs * kN;
+    static_assert(kColL + kOBufs * kN <= kTmemCols, "tensor memory");
+};
+
+constexpr int kMaxStages = 10;
+
+struct Ctl {
+    unsigned long long kv_full[kMaxStages], kv_empty[kMaxStages];
+    unsigned long long s_full[2], p_full[2], p_free[2];
+    unsigned long long q_full[2], q_empty[2], o_full[2], o_empty[2], drain;
+    long long start_off;                          // first tile's place in its request
+    unsigned long long sums[kThreads / 32];
+    int start_b;
+    uint32_t tmem;
+    int abort;
+    int odd[2];                                   // a cleared value, by parity of the segment
+};
+
+template <int D, int kN>
+constexpr int smem_bytes()
+{
+    static_assert(Cfg<D, kN>::kCtl + sizeof(Ctl) <= 227 * 1024, "shared memory of a CTA");
+    return Cfg<D, kN>::kCtl + static_cast<int>(sizeof(Ctl));
+}
+
+// Rows and context of request b, inside the arrays and the block table.
+__device__ __forceinline__ void load_request(const Params &p, int b, int &ctx, int &rows, int &start,
+                                             bool &bad)
+{
+    const int s0 = p.row_start[b], s1 = p.row_start[b + 1], c = p.context[b];
+    start = min(max(s0, 0), p.row_capacity);
+    rows = min(max(s1, start), p.row_capacity) - start;
+    const int room = static_cast<int>(
+        min(static_cast<long long>(p.max_pages) * p.ps, static_cast<long long>(INT32_MAX)));
+    bad = s0 != start || s1 != start + rows;
+    ctx = max(c, 0);
+    if (rows > room || ctx > room - rows) {
+        bad = true;
+        rows = min(rows, room);
+        ctx = room - rows;
     }
-    const int b = lo;
-    const size_t at = (static_cast<size_t>(row) * p.Hq + h) * D;
-    if (tid < D) q_s[tid] = __uint_as_float(static_cast<uint32_t>(p.q[at + tid]) << 16);
+}
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Ctl &ctl, const Params &p)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_try_wait_sleep(bar, parity, kWaitHintNs)) return true;
+        if (*reinterpret_cast<volatile int *>(&ctl.abort)) return false;
+        if (globaltimer_ns() - t0 > p.timeout_ns) {
+            record_error(DSPARK_TIMEOUT);
+            *reinterpret_cast<volatile int *>(&ctl.abort) = 1;
+            return false;
+        }
+    }
+}
+
+// The same for a whole warp, which goes on only if every lane may.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, Ctl &ctl, const Params &p)
+{
+    return __all_sync(0xFFFFFFFFu, wait(bar, parity, ctl, p));
+}
+
+// Bounded wait for this CTA's own copies and MMAs before it ends, whatever the abort flag.
+__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const Params &p)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_sleep(bar, parity, kWaitHintNs))
+        if (globaltimer_ns() - t0 > p.timeout_ns) {
+            record_error(DSPARK_TIMEOUT);
+            return;
+        }
+}
+
+// A CTA's way along its tiles, segment (part of a unit) by segment.  Every role walks it by
+// itself, a whole warp at a time: the lanes hold the next 32 requests' lengths.
+struct Walk {
+    int base, l_ctx, l_rows, l_start;             // request base + lane
+    int b, ctx, rows, start;
+    int h, qt, kt, kt_end, tiles;                 // segment [kt, kt_end) of the unit's tiles
+    long long left;
+
+    __device__ __forceinline__ void load(const Params &p)
+    {
+        const int r = base + static_cast<int>(threadIdx.x & 31);
+        l_ctx = l_rows = l_start = 0;
+        bool bad;
+        if (r < p.B) load_request(p, r, l_ctx, l_rows, l_start, bad);
+    }
+    __device__ __forceinline__ void take(int request)
+    {
+        b = request;
+        ctx = __shfl_sync(0xFFFFFFFFu, l_ctx, b - base);
+        rows = __shfl_sync(0xFFFFFFFFu, l_rows, b - base);
+        start = __shfl_sync(0xFFFFFFFFu, l_start, b - base);
+    }
+    __device__ __forceinline__ vplan::Request request(const Params &p) const
+    {
+        return vplan::Request{ctx, rows, p.tokens};
+    }
+    __device__ __forceinline__ void segment(const Params &p)
+    {
+        tiles = request(p).key_tiles(qt);
+        const long long n = min(static_cast<long long>(tiles - kt), left);
+        kt_end = kt + static_cast<int>(n);
+        left -= n;
+    }
+    // The segment at tile `off` of request b0; false when there is none.
+    __device__ __forceinline__ bool begin(const Params &p, int b0, long long off, long long count)
+    {
+        left = count;
+        if (count <= 0) return false;
+        base = b0;
+        load(p);
+        take(b0);
+        place(request(p), off, h, qt, kt);
+        segment(p);
+        return true;
+    }
+    __device__ __forceinline__ bool next(const Params &p)
+    {
+        if (left <= 0) return false;
+        kt = 0;
+        if (++qt == request(p).query_tiles()) {
+            qt = 0;
+            if (++h == p.Hkv) {
+                h = 0;
+                unsigned more = __ballot_sync(
+                    0xFFFFFFFFu, l_rows > 0 && base + static_cast<int>(threadIdx.x & 31) > b);
+                while (!more) {
+                    base += 32;
+                    if (base >= p.B) return false;
+                    load(p);
+                    more = __ballot_sync(0xFFFFFFFFu, l_rows > 0);
+                }
+                take(base + __ffs(more) - 1);
+            }
+        }
+        segment(p);
+        return true;
+    }
+    __device__ __forceinline__ int first_token(const Params &p) const { return qt * p.tokens; }
+    // rows of the unit (tokens times query heads) and keys that it sees
+    __device__ __forceinline__ int unit_rows(const Params &p) const
+    {
+        return min(rows - qt * p.tokens, p.tokens) * p.group;
+    }
+    __device__ __forceinline__ int keys(const Params &p) const { return request(p).keys(qt); }
+};
+
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+
+__device__ __forceinline__ bool soft_any(bool v)
+{
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return any != 0;
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t &a, uint32_t &b, uint32_t &c,
+                                       uint32_t &d)
+{
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+                 : "r"(addr)
+                 : "memory");
+}
+
+// Maximum of each of 16 columns over the warp's 32 lanes, halving the columns that a lane
+// holds at every exchange: 16 shuffles.  Lane t ends with column t / 2.
+__device__ __forceinline__ float column_max(float (&v)[16])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) {
+        const int bit = 2 * w;
+        const bool up = lane & bit;
+#pragma unroll
+        for (int k = 0; k < w; ++k) {
+            const float keep = up ? v[k + w] : v[k], send = up ? v[k] : v[k + w];
+            v[k] = fmaxf(keep, __shfl_xor_sync(0xFFFFFFFFu, send, bit));
+        }
+    }
+    return fmaxf(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
+}
+
+__device__ __forceinline__ bool not_finite(uint32_t w)   // either bf16 of a word
+{
+    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w)
+{
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0xFFFFu;
+    return w;
+}
+
+template <int D, int kN>
+__global__ void __launch_bounds__(kThreads, 1)
+    verify_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v, const Params p)
+{
+    using C = Cfg<D, kN>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t s0 = smem_u32(smem);
+    Ctl &ctl = *reinterpret_cast<Ctl *>(smem + C::kCtl);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    launch_dependents();
+    if (s0 % 1024 != 0) {                         // the swizzled tiles need it
+        if (tid == 0) record_error(DSPARK_BAD_LAUNCH);
+        if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return;
+    }
+
+    // ------------------------------------------------ this CTA's share of the tiles
+    long long mine = 0;
+    const int per = (p.B + kThreads - 1) / kThreads, r0 = tid * per;
+    for (int r = r0; r < min(r0 + per, p.B); ++r) {
+        int ctx, rows, start;
+        bool bad;
+        load_request(p, r, ctx, rows, start, bad);
+        if (bad && blockIdx.x == 0) record_error(DSPARK_INVALID_TOKEN);
+        if (rows > 0) mine += vplan::Request{ctx, rows, p.tokens}.per_head() * p.Hkv;
+    }
+    long long sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += u;
+    }
+    if (lane == 31) ctl.sums[warp] = sum;
+    for (int i = tid; i < kOnesBytes / 4; i += kThreads)
+        reinterpret_cast<uint32_t *>(smem + C::kOnes)[i] = 0x3F803F80u;
+    const uint32_t kv_full = smem_u32(ctl.kv_full), kv_empty = smem_u32(ctl.kv_empty);
+    const uint32_t s_full = smem_u32(ctl.s_full), p_full = smem_u32(ctl.p_full);
+    const uint32_t p_free = smem_u32(ctl.p_free), q_full = smem_u32(ctl.q_full);
+    const uint32_t q_empty = smem_u32(ctl.q_empty), o_full = smem_u32(ctl.o_full);
+    const uint32_t o_empty = smem_u32(ctl.o_empty), drain = smem_u32(&ctl.drain);
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(kv_full + 8 * i, 1);
+            mbar_init(kv_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, kSoftThreads);
+            mbar_init(p_free + 8 * i, 1);
+            mbar_init(q_full + 8 * i, kQThreads);
+            mbar_init(q_empty + 8 * i, 1);
+            mbar_init(o_full + 8 * i, 1);
+            mbar_init(o_empty + 8 * i, kSoftThreads);
+        }
+        mbar_init(drain, 1);
+        mbar_fence_init();
+        ctl.abort = 0;
+        ctl.odd[0] = ctl.odd[1] = 0;
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
+        tmem_relinquish();
+    }
     __syncthreads();
-    const int kvh = h / (p.Hq / p.Hkv);
-    const long long room = static_cast<long long>(p.max_pages) * p.ps;
-    const long long wants = static_cast<long long>(max(p.context[b], 0)) + row - p.row_start[b] + 1;
-    if (wants > room) record_error(DSPARK_INVALID_TOKEN);
-    const int len = static_cast<int>(min(wants, room));
-    float m = -INFINITY, l = 0.0f, acc = 0.0f;
-    for (int j0 = 0; j0 < len; j0 += kThreads) {
-        const int j = j0 + tid;
-        float s = -INFINITY;
-        if (j < len) {
-            int page = p.pages[static_cast<size_t>(b) * p.max_pages + j / p.ps];
+    long long T = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += ctl.sums[w];
+        T += ctl.sums[w];
+    }
+    before += sum - mine;
+    const int G = vplan::ctas(T, gridDim.x);
+    const int cta = blockIdx.x;
+    const long long t0 = cta < G ? vplan::first_tile(T, cta, G) : 0;
+    const long long t1 = cta < G ? vplan::first_tile(T, cta + 1, G) : 0;
+    if (t1 > t0 && before <= t0 && t0 < before + mine) {
+        long long at = before;
+        for (int r = r0; r < min(r0 + per, p.B); ++r) {
+            int ctx, rows, start;
+            bool bad;
+            load_request(p, r, ctx, rows, start, bad);
+            const long long n =
+                rows > 0 ? vplan::Request{ctx, rows, p.tokens}.per_head() * p.Hkv : 0;
+            if (t0 < at + n) {
+                ctl.start_b = r;
+                ctl.start_off = t0 - at;
+                break;
+            }
+            at += n;
+        }
+    }
+    fence_proxy_async_smem();                     // the ones
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    Walk w;
+    bool more = w.begin(p, t1 > t0 ? ctl.start_b : 0, t1 > t0 ? ctl.start_off : 0, t1 - t0);
+
+    if (warp == kWarpLoad) {
+        // ---------------------------------------------------- K and V pages into the ring
+        const int boxes = kTileKeys / p.ps;       // pages of a tile
+        uint32_t issued = 0;
+        bool ok = true;
+        // page ids one tile ahead of the copies
+        auto page_of = [&](int kt, int keys) {
+            const int key = kt * kTileKeys + lane * p.ps;
+            if (lane >= boxes || key >= keys) return -1;
+            int page = p.pages[static_cast<size_t>(w.b) * p.max_pages + key / p.ps];
             if (page < 0 || page >= p.num_pages) {
                 record_error(DSPARK_INVALID_PAGE);
                 page = 0;
             }
-            const size_t off = ((static_cast<size_t>(page) * p.Hkv + kvh) * p.ps + j % p.ps) * D;
-            const uint4 *k = reinterpret_cast<const uint4 *>(p.k_cache + off);
-            v_s[tid] = p.v_cache + off;
-            s = 0.0f;
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 w = k[c];
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            return page;
+        };
+        int kt = w.kt;
+        int page = more ? page_of(kt, w.keys(p)) : -1;
+        while (more && ok) {
+            const int h = w.h, cur = page;
+            if (++kt < w.kt_end) {
+                page = page_of(kt, w.keys(p));
+            } else {
+                more = w.next(p);
+                kt = w.kt;
+                page = more ? page_of(kt, w.keys(p)) : -1;
+            }
+            const int live = __popc(__ballot_sync(0xFFFFFFFFu, cur >= 0));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s = fmaf(bf16lo_to_f32(u[e]), q_s[8 * c + 2 * e], s);
-                    s = fmaf(bf16hi_to_f32(u[e]), q_s[8 * c + 2 * e + 1], s);
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t slot = issued % C::kStages;
+                const uint32_t parity = ((issued / C::kStages) & 1u) ^ 1u;
+                if (!warp_wait(kv_empty + 8 * slot, parity, ctl, p)) {
+                    ok = false;
+                    break;
+                }
+                __syncwarp();
+                const uint32_t bar = kv_full + 8 * slot;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(live) * p.ps * D * 2);
+                __syncwarp();
+                if (cur >= 0) {
+                    const uint32_t dst = s0 + C::kRing + slot * C::kTileBytes + lane * p.ps * 128;
+                    const int row = (cur * p.Hkv + h) * p.ps;
+                    const void *map = kv ? &tm_v : &tm_k;
+                    tma_load_2d_plain(dst, map, bar, 0, row);
+                    if (D == 128) tma_load_2d_plain(dst + C::kHalfBytes, map, bar, 64, row);
+                }
+                ++issued;
+            }
+        }
+        for (uint32_t s = 0; s < C::kStages; ++s) {   // copies land before the CTA ends
+            const uint32_t uses = issued / C::kStages + (s < issued % C::kStages ? 1 : 0);
+            if (uses > 0) wait_drain(kv_full + 8 * s, (uses - 1) & 1u, p);
+        }
+    } else if (warp == kWarpMma) {
+        // ---------------------------------------------------- S^T = K Q^T, O^T += V^T P
+        const uint64_t ones = smem_desc(s0 + C::kOnes, 128, 128, kSwizzleNone);
+        struct Tile {
+            uint32_t n;                           // columns
+            uint32_t seg;
+            bool first, last;
+        } prev = {0, 0, false, false};
+        uint32_t i = 0, seg = 0;
+        bool ok = true, any = false;
+        auto values = [&](const Tile &t, uint32_t j) {
+            const uint32_t slot = (2 * j + 1) % C::kStages;
+            const uint32_t pb = j % C::kPBufs, ob = t.seg % C::kOBufs;
+            if (!warp_wait(kv_full + 8 * slot, ((2 * j + 1) / C::kStages) & 1u, ctl, p))
+                return false;
+            if (t.first && !warp_wait(o_empty + 8 * ob,
+                                 ((t.seg / C::kOBufs) & 1u) ^ 1u, ctl, p))
+                return false;
+            if (!warp_wait(p_full + 8 * (j & 1), (j >> 1) & 1u, ctl, p))
+                return false;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint64_t a = smem_desc(s0 + C::kRing + slot * C::kTileBytes, C::kHalfBytes,
+                                             1024, kSwizzle128B);
+                const uint64_t b = smem_desc(s0 + C::kP + pb * C::kPBytes, kTileKeys * 128, 1024,
+                                             kSwizzle128B);
+                const uint32_t id_o = idesc_bf16_f32(D, t.n, 1, 1);
+                const uint32_t id_l = idesc_bf16_f32(64, t.n, 0, 1);
+#pragma unroll
+                for (int k = 0; k < kTileKeys / 16; ++k) {
+                    const uint32_t acc = !t.first || k > 0;
+                    umma_bf16(tmem + C::kColO + ob * kN, a + k * 128, b + k * 128, id_o, acc);
+                    umma_bf16(tmem + C::kColL + ob * kN, ones, b + k * 128, id_l, acc);
+                }
+                umma_commit(kv_empty + 8 * slot);
+                umma_commit(p_free + 8 * pb);
+                if (t.last) umma_commit(o_full + 8 * ob);
+            }
+            __syncwarp();
+            return true;
+        };
+        while (more && ok) {
+            const uint32_t n = (w.unit_rows(p) + 15) & ~15;
+            for (int kt = w.kt; kt < w.kt_end && ok; ++kt) {
+                const bool first = kt == w.kt, last = kt + 1 == w.kt_end;
+                const uint32_t slot = (2 * i) % C::kStages, qb = seg % C::kQBufs;
+                ok = (!first || warp_wait(q_full + 8 * qb, (seg / C::kQBufs) & 1u,
+                                     ctl, p)) &&
+                     warp_wait(kv_full + 8 * slot, ((2 * i) / C::kStages) & 1u, ctl,
+                          p);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t a = smem_desc(s0 + C::kRing + slot * C::kTileBytes, 16, 1024,
+                                                 kSwizzle128B);
+                    const uint64_t b = smem_desc(s0 + C::kQ + qb * C::kQBytes, 16, 1024,
+                                                 kSwizzle128B);
+                    const uint32_t id = idesc_bf16_f32(kTileKeys, n, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        umma_bf16(tmem + C::kColS + (i & 1) * kN,
+                                  a + (k >> 2) * (C::kHalfBytes >> 4) + (k & 3) * 2,
+                                  b + (k >> 2) * (kN * 128 >> 4) + (k & 3) * 2, id, k > 0);
+                    umma_commit(kv_empty + 8 * slot);
+                    umma_commit(s_full + 8 * (i & 1));
+                    if (last) umma_commit(q_empty + 8 * qb);
+                }
+                __syncwarp();
+                any = true;
+                if (i > 0) ok = values(prev, i - 1);
+                prev = Tile{n, seg, first, last};
+                ++i;
+            }
+            ++seg;
+            more = w.next(p);
+        }
+        if (ok && i > 0) values(prev, i - 1);
+        if (any) {                                // MMAs finish before the CTA ends
+            if (lane == 0) umma_commit(drain);
+            __syncwarp();
+            wait_drain(drain, 0, p);
+        }
+    } else if (warp >= kWarpQ) {
+        // ---------------------------------------------------- Q rows of each segment
+        const int t = tid - kWarpQ * 32;
+        uint32_t seg = 0;
+        while (more) {
+            const uint32_t qb = seg % C::kQBufs;
+            const int rows = w.unit_rows(p), n = (rows + 15) & ~15;
+            if (!warp_wait(q_empty + 8 * qb, ((seg / C::kQBufs) & 1u) ^ 1u, ctl, p))
+                break;
+            const uint32_t dst = s0 + C::kQ + qb * C::kQBytes;
+            const size_t row0 = static_cast<size_t>(w.start + w.first_token(p)) * p.Hq +
+                                static_cast<size_t>(w.h) * p.group;
+            for (int c = t; c < n * (D / 8); c += kQThreads) {
+                const int r = c / (D / 8), u = c % (D / 8);
+                const uint32_t to = dst + (u >> 3) * (kN * 128) + r * 128 +
+                                    (((u & 7) ^ (r & 7)) << 4);
+                if (r < rows) {
+                    const size_t row = row0 + static_cast<size_t>(r / p.group) * p.Hq + r % p.group;
+                    cp_async_16(to, p.q + row * D + u * 8);
+                } else {
+                    sts128(to, 0, 0, 0, 0);
                 }
             }
-            s *= p.scale;
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            mbar_arrive(q_full + 8 * qb);
+            ++seg;
+            more = w.next(p);
         }
-        float t = s;
+    } else {
+        // ---------------------------------------------------- softmax and output
+        float *m_s = reinterpret_cast<float *>(smem + C::kM);
+        float *red = reinterpret_cast<float *>(smem + C::kRed);
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        // the output's channel of this thread (M = 64 puts 16 rows in each warp's lanes)
+        const int d = D == 128 ? tid : warp * 16 + (lane & 15);
+        const bool has_d = D == 128 || lane < 16;
+        const float sl = p.scale_log2;
+        struct Seg {
+            int row0, rows, h, kt, kt_end, keys, hidden, b;   // hidden: keys that row 0 sees
+            bool starts, ends;
+            int parts;
+        } cur = {}, done = {};
+        int4 desc = make_int4(0, 0, 0, 0);
+
+        // after a wait that ran out the warps go on without waiting, so that they meet at the
+        // same barriers until the end (the results are unspecified then)
+        bool dead = false;
+        auto await = [&](uint32_t bar, uint32_t parity) {
+            if (!dead && !wait(bar, parity, ctl, p)) dead = true;
+        };
+
+        // l, O -> out, or to the workspace when the unit has other parts
+        auto output = [&](const Seg &s, uint32_t seg) {
+            const uint32_t ob = seg % C::kOBufs;
+            await(o_full + 8 * ob, (seg / C::kOBufs) & 1u);
+            __syncwarp();
+            tc_fence_after();
+            const bool direct = s.starts && s.ends;
+            const int part = 2 * blockIdx.x + (s.starts ? 1 : 0);
+            const bool odd = *reinterpret_cast<volatile int *>(&ctl.odd[seg & 1]);
+            for (int c0 = 0; c0 < s.rows; c0 += 16) {
+                uint32_t o[16], l[16];
+                tmem_ld_32x32b_x16(lane_base + C::kColO + ob * kN + c0, o);
+                tmem_ld_32x32b_x16(lane_base + C::kColL + ob * kN + c0, l);
+                tmem_wait_ld16(o);
+                tmem_wait_ld16(l);
+                float v[16];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
-        if ((tid & 31) == 0) red[tid >> 5] = t;
-        __syncthreads();
-        t = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), m);
-        const float f = m == -INFINITY ? 0.0f : expf(m - t);
-        m = t;
-        const float e = j < len ? expf(s - m) : 0.0f;
-        p_s[tid] = e;
-        const float w = warp_sum(e);
-        __syncthreads();
-        if ((tid & 31) == 0) red[tid >> 5] = w;
-        __syncthreads();
-        l = l * f + (red[0] + red[1]) + (red[2] + red[3]);
-        if (tid < D) {
-            acc *= f;
-            for (int i = 0; i < min(kThreads, len - j0); ++i)
-                acc = fmaf(p_s[i], __uint_as_float(static_cast<uint32_t>(v_s[i][tid]) << 16), acc);
+                for (int j = 0; j < 16; ++j) {
+                    l[j] = __shfl_sync(0xFFFFFFFFu, l[j], 0);
+                    v[j] = __uint_as_float(o[j]);
+                    if (direct) v[j] *= 1.0f / __uint_as_float(l[j]);
+                }
+                if (odd && has_d) {               // values that are not finite, to who sees them
+                    for (int j = max(s.kt * kTileKeys, s.hidden); j < min(s.kt_end * kTileKeys, s.keys);
+                         ++j) {
+                        int page = p.pages[static_cast<size_t>(s.b) * p.max_pages + j / p.ps];
+                        if (page < 0 || page >= p.num_pages) page = 0;
+                        const uint32_t x =
+                            p.v_cache[((static_cast<size_t>(page) * p.Hkv + s.h) * p.ps +
+                                       j % p.ps) * D + d];
+                        if ((x & 0x7F80u) == 0x7F80u) {
+                            const int from = (j - s.hidden + 1) * p.group;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (c0 + e >= from) v[e] += __uint_as_float(x << 16);
+                        }
+                    }
+                }
+                if (direct) {
+                    // neighbouring lanes hold neighbouring channels: the even lane stores row
+                    // j's pair, the odd lane row j + 1's
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const bool up = lane & 1;
+                        const float got =
+                            __shfl_xor_sync(0xFFFFFFFFu, up ? v[j] : v[j + 1], 1);
+                        const uint32_t word =
+                            up ? pack2_bf16(got, v[j + 1]) : pack2_bf16(v[j], got);
+                        const int r = c0 + j + (up ? 1 : 0);
+                        if (r < s.rows && has_d) {
+                            const size_t row = static_cast<size_t>(s.row0 + r / p.group) * p.Hq +
+                                               static_cast<size_t>(s.h) * p.group + r % p.group;
+                            *reinterpret_cast<uint32_t *>(p.out + row * D + (d & ~1)) = word;
+                        }
+                    }
+                } else {
+                    float *to = p.part_o + (static_cast<size_t>(part) * kMaxRows + c0) * D + d;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (c0 + j >= s.rows) break;
+                        if (has_d) to[j * D] = v[j];
+                        if (tid == 0)
+                            p.part_ml[static_cast<size_t>(part) * kMaxRows + c0 + j] =
+                                make_float2(m_s[(seg & 1) * kN + c0 + j], __uint_as_float(l[j]));
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(o_empty + 8 * ob);
+        };
+
+        // the tile's scores times scale log2(e), hidden ones -inf
+        auto scores = [&](uint32_t (&r)[16], float (&t)[16], int c0, int from) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                t[j] = __uint_as_float(r[j]) * sl;
+                if (c0 + j < from) t[j] = -INFINITY;
+            }
+        };
+        // red[.][row] = the tile's maximum in each warp's keys
+        auto reduce = [&](uint32_t col, int n, int from) {
+            for (int c0 = 0; c0 < n; c0 += 16) {
+                uint32_t r[16];
+                float t[16];
+                tmem_ld_32x32b_x16(col + c0, r);
+                tmem_wait_ld16(r);
+                scores(r, t, c0, from);
+                const float m = column_max(t);
+                if ((lane & 1) == 0) red[warp * kN + c0 + (lane >> 1)] = m;
+            }
+        };
+        auto max_of = [&](int r) {
+            return fmaxf(fmaxf(red[r], red[kN + r]), fmaxf(red[2 * kN + r], red[3 * kN + r]));
+        };
+
+        uint32_t i = 0, seg = 0;
+        while (more) {
+            const int tok0 = w.first_token(p);
+            cur.row0 = w.start + tok0;
+            cur.rows = w.unit_rows(p);
+            cur.h = w.h;
+            cur.b = w.b;
+            cur.kt = w.kt;
+            cur.kt_end = w.kt_end;
+            cur.keys = w.keys(p);
+            cur.hidden = w.ctx + tok0 + 1;
+            cur.starts = w.kt == 0;
+            cur.ends = w.kt_end == w.tiles;
+            if (cur.starts && !cur.ends)
+                desc = make_int4(cur.row0, cur.h, cur.rows,
+                                 vplan::cta_of(T, t1 - 1 + (w.tiles - w.kt_end), G) - cta + 1);
+            const int n = (cur.rows + 15) & ~15;
+            float *m_row = m_s + (seg & 1) * kN;
+            for (int kt = cur.kt; kt < cur.kt_end; ++kt) {
+                const uint32_t col = lane_base + C::kColS + (i & 1) * kN;
+                const int key = kt * kTileKeys + tid;
+                // rows from `from` on see this thread's key
+                int from = 0;
+                if (key >= cur.keys) from = kMaxRows;
+                else if (key >= cur.hidden) from = (key - cur.hidden + 1) * p.group;
+                await(s_full + 8 * (i & 1), (i >> 1) & 1u);
+                __syncwarp();
+                tc_fence_after();
+                if (kt == cur.kt) {               // m: the maximum over the first tile
+                    reduce(col, n, from);
+                    soft_sync();
+                    if (tid < n) {
+                        const float m = max_of(tid);
+                        m_row[tid] = m == -INFINITY ? 0.0f : m;
+                    }
+                    if (tid == 0) ctl.odd[seg & 1] = 0;
+                    soft_sync();
+                }
+                if ((kt + 1) * kTileKeys > cur.hidden) {
+                    // values behind the last key, and those that are not finite
+                    const uint32_t slot = (2 * i + 1) % C::kStages;
+                    await(kv_full + 8 * slot, ((2 * i + 1) / C::kStages) & 1u);
+                    if (from > 0) {
+                        const uint32_t v = s0 + C::kRing + slot * C::kTileBytes + tid * 128;
+                        bool odd = false;
+                        for (int u = 0; u < D / 8; ++u) {
+                            const uint32_t at = v + (u >> 3) * C::kHalfBytes + ((u & 7) << 4);
+                            uint32_t x0 = 0, x1 = 0, x2 = 0, x3 = 0;
+                            if (key < cur.keys) {
+                                lds128(at, x0, x1, x2, x3);
+                                if (!not_finite(x0) && !not_finite(x1) && !not_finite(x2) &&
+                                    !not_finite(x3))
+                                    continue;
+                                odd = true;
+                                x0 = finite_or_zero(x0);
+                                x1 = finite_or_zero(x1);
+                                x2 = finite_or_zero(x2);
+                                x3 = finite_or_zero(x3);
+                            }
+                            sts128(at, x0, x1, x2, x3);
+                        }
+                        if (odd) *reinterpret_cast<volatile int *>(&ctl.odd[seg & 1]) = 1;
+                    }
+                }
+                const uint32_t pb = i % C::kPBufs;
+                await(p_free + 8 * pb, ((i / C::kPBufs) & 1u) ^ 1u);
+                __syncwarp();
+                const uint32_t prow = s0 + C::kP + pb * C::kPBytes + tid * 128;
+                // weights to shared memory; the largest log2 of one
+                auto weights = [&]() {
+                    float top = -INFINITY;
+                    for (int c0 = 0; c0 < n; c0 += 16) {
+                        uint32_t r[16];
+                        float t[16];
+                        tmem_ld_32x32b_x16(col + c0, r);
+                        const float4 *m4 = reinterpret_cast<const float4 *>(m_row + c0);
+                        float m[16];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float4 x = m4[q];
+                            m[4 * q] = x.x, m[4 * q + 1] = x.y, m[4 * q + 2] = x.z,
+                                  m[4 * q + 3] = x.w;
+                        }
+                        tmem_wait_ld16(r);
+                        uint32_t word[8];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            t[j] = fmaf(__uint_as_float(r[j]), sl, -m[j]);
+                            if (c0 + j < from) t[j] = -INFINITY;
+                            top = fmaxf(top, t[j]);
+                            t[j] = exp2_approx(t[j]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) word[j] = pack2_bf16(t[2 * j], t[2 * j + 1]);
+                        const uint32_t to = prow + (c0 >> 6) * (kTileKeys * 128);
+                        const int u = (c0 >> 3) & 7;
+                        sts128(to + ((u ^ (tid & 7)) << 4), word[0], word[1], word[2], word[3]);
+                        sts128(to + (((u + 1) ^ (tid & 7)) << 4), word[4], word[5], word[6], word[7]);
+                    }
+                    return top;
+                };
+                if (soft_any(weights() > kRaise)) {
+                    // m rises: O and l of the tiles before are scaled, the weights made anew
+                    reduce(col, n, from);
+                    soft_sync();
+                    if (tid < n) {
+                        const float old = m_row[tid], now = fmaxf(old, max_of(tid));
+                        m_row[tid] = now;
+                        red[tid] = exp2_approx(old - now);
+                    }
+                    soft_sync();
+                    const uint32_t ob = seg % C::kOBufs;
+                    if (kt > cur.kt)
+                        await(p_free + 8 * ((i - 1) % C::kPBufs), ((i - 1) / C::kPBufs) & 1u);
+                    __syncwarp();
+                    tc_fence_after();
+                    for (int c0 = 0; kt > cur.kt && c0 < n; c0 += 16) {
+                        for (uint32_t base : {C::kColO, C::kColL}) {
+                            uint32_t r[16];
+                            tmem_ld_32x32b_x16(lane_base + base + ob * kN + c0, r);
+                            tmem_wait_ld16(r);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                r[j] = __float_as_uint(__uint_as_float(r[j]) * red[c0 + j]);
+                            tmem_st_32x32b_x16(lane_base + base + ob * kN + c0, r);
+                        }
+                    }
+                    tmem_wait_st();
+                    weights();
+                    soft_sync();                  // red is free again
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(p_full + 8 * (i & 1));
+                ++i;
+                if (kt == cur.kt && seg > 0) output(done, seg - 1);
+            }
+            done = cur;
+            ++seg;
+            more = w.next(p);
         }
-        __syncthreads();
+        if (seg > 0) output(done, seg - 1);
+        if (tid == 0) p.desc[blockIdx.x] = desc;
     }
-    if (tid < D) {
-        const __nv_bfloat16 o = __float2bfloat16_rn(acc / l);
-        p.out[at + tid] = *reinterpret_cast<const uint16_t *>(&o);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Adds up the parts of the unit that starts in CTA blockIdx.x and ends in a later one: with
+// M = max m,  out = sum 2^(m - M) O / sum 2^(m - M) l.  A warp takes a row at a time.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) verify_join_kernel(const Params p)
+{
+    constexpr int kPer = D / 32;
+    wait_for_prior_kernels();
+    const int4 unit = p.desc[blockIdx.x];
+    const int row0 = unit.x, h = unit.y, rows = unit.z, parts = unit.w;
+    if (parts < 2) return;
+    const int lane = threadIdx.x & 31;
+    for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
+         r += kJoinSplit * (kJoinThreads / 32)) {
+        // part 0 is its CTA's last, the others their CTAs' first
+        auto part = [&](int i) {
+            return static_cast<size_t>(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kMaxRows + r;
+        };
+        float m = -INFINITY;
+        for (int i = lane; i < parts; i += 32) {
+            const float2 x = p.part_ml[part(i)];
+            if (x.y > 0.0f || x.y != x.y) m = fmaxf(m, x.x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        float l = 0.0f, acc[kPer] = {};
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i) {
+            const float2 x = p.part_ml[part(i)];
+            if (x.y == 0.0f) continue;            // no key of this part is seen
+            const float f = exp2_approx(x.x - m);
+            l = fmaf(x.y, f, l);
+            const float *o = p.part_o + part(i) * D + lane * kPer;
+            if (kPer == 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(o);
+                acc[0] = fmaf(v.x, f, acc[0]);
+                acc[1] = fmaf(v.y, f, acc[1]);
+                acc[2 % kPer] = fmaf(v.z, f, acc[2 % kPer]);
+                acc[3 % kPer] = fmaf(v.w, f, acc[3 % kPer]);
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(o);
+                acc[0] = fmaf(v.x, f, acc[0]);
+                acc[1] = fmaf(v.y, f, acc[1]);
+            }
+        }
+        const float inv = 1.0f / l;
+        uint32_t *to = reinterpret_cast<uint32_t *>(
+            p.out + (static_cast<size_t>(row0 + r / p.group) * p.Hq +
+                     static_cast<size_t>(h) * p.group + r % p.group) * D + lane * kPer);
+#pragma unroll
+        for (int j = 0; j < kPer; j += 2) to[j / 2] = pack2_bf16(acc[j] * inv, acc[j + 1] * inv);
     }
 }
 

@@ -1,0 +1,100 @@
+// verify_plan.h -- how the attention of a verification batch is cut into work for the CTAs.
+//
+// A unit is (request, key head, query tile): up to `tokens` of the request's rows, all the
+// query heads of one key head, against the keys that the tile's last row sees, in key tiles
+// of 128.  All units' key tiles stand in one line (requests, then key heads, then query
+// tiles), and CTA c of G takes the tiles from floor(T c / G) to floor(T (c + 1) / G) of the
+// T: equal work whatever the lengths, a function of the lengths alone.  A unit cut by a
+// border is joined from its parts.
+//
+// Plain integer arithmetic, the same on the host and the device.
+#pragma once
+
+#ifdef __CUDACC__
+#define DSPARK_HD __host__ __device__ __forceinline__
+#else
+#define DSPARK_HD inline
+#endif
+
+namespace dspark {
+namespace vplan {
+
+constexpr int kTileKeys = 128;
+
+// sum over i = 0 .. n - 1 of floor((a i + b) / 2^7), a, b >= 0, by Euclid's steps
+DSPARK_HD long long floor_sum(long long n, long long a, long long b)
+{
+    long long m = kTileKeys, sum = 0;
+    while (true) {
+        if (a >= m) {
+            sum += n * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            sum += n * (b / m);
+            b %= m;
+        }
+        const long long top = a * n + b;
+        if (top < m) return sum;
+        n = top / m;
+        b = top % m;
+        const long long t = m;
+        m = a;
+        a = t;
+    }
+}
+
+struct Request {
+    int ctx, rows;     // rows > 0
+    int tokens;        // rows of a query tile
+
+    DSPARK_HD int query_tiles() const { return (rows + tokens - 1) / tokens; }
+    // keys that query tile qt sees, and its key tiles
+    DSPARK_HD int keys(int qt) const
+    {
+        const long long end = (static_cast<long long>(qt) + 1) * tokens;
+        return ctx + static_cast<int>(end < rows ? end : rows);
+    }
+    DSPARK_HD int key_tiles(int qt) const { return (keys(qt) - 1) / kTileKeys + 1; }
+    // key tiles of query tiles 0 .. qt - 1, all but the last of which may be full
+    DSPARK_HD long long before(int qt) const
+    {
+        if (qt <= 0) return 0;
+        const int full = qt < query_tiles() ? qt : query_tiles() - 1;
+        long long sum = full > 0 ? floor_sum(full, tokens, static_cast<long long>(ctx) + tokens +
+                                                               kTileKeys - 1)
+                                 : 0;
+        if (full < qt) sum += key_tiles(full);
+        return sum;
+    }
+    DSPARK_HD long long per_head() const { return before(query_tiles()); }
+};
+
+// first key tile of CTA c of G
+DSPARK_HD long long first_tile(long long T, int c, int G) { return T * c / G; }
+// the CTA that holds tile t
+DSPARK_HD int cta_of(long long T, long long t, int G)
+{
+    return static_cast<int>(((t + 1) * G - 1) / T);
+}
+// CTAs that take part: each has at least one tile
+DSPARK_HD int ctas(long long T, int most) { return T < most ? static_cast<int>(T) : most; }
+
+// Place of tile `at` of a request with per_head() * heads tiles: key head, query tile, key tile.
+DSPARK_HD void place(const Request &r, long long at, int &h, int &qt, int &kt)
+{
+    const long long per = r.per_head();
+    h = static_cast<int>(at / per);
+    const long long rest = at - h * per;
+    int lo = 0, hi = r.query_tiles() - 1;
+    while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (r.before(mid) <= rest) lo = mid;
+        else hi = mid - 1;
+    }
+    qt = lo;
+    kt = static_cast<int>(rest - r.before(lo));
+}
+
+}  // namespace vplan
+}  // namespace dspark
