@@ -112,6 +112,21 @@ __device__ __forceinline__ void fence_proxy_async_smem()
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// True in one lane of the (whole, converged) warp.  Inside the branch the compiler knows that
+// one thread runs, and moves descriptors and addresses to uniform registers directly; under a
+// plain `lane == 0` it wraps every tcgen05 and TMA instruction in a loop over the warp's values
+// (measured: 40 instead of 140 cycles per MMA of 16 columns).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const void *desc)
 {

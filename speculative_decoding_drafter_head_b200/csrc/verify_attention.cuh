@@ -32,9 +32,10 @@
 // border leave (m, l, O) in the workspace, and verify_join_kernel adds the parts up, in
 // order, so results do not depend on timing.  It is launched to overlap with this kernel's end.
 //
-// Warps: 0-3 softmax and output (thread = key of the tile, then channel of the output), 4
-// copies K and V pages into a ring of 32 KB tiles by TMA (one box a page), 5 issues the MMAs,
-// 6 and 7 copy Q.  S and P are double-buffered, so S of the next tile and O of the last run
+// Warps: 0-3 softmax and output (thread = key of the tile, then channel of the output), 4 and
+// 5 copy K and V pages into a ring of 32 KB tiles by TMA (one box a page and 64 channels; one
+// warp for both took 90 cycles a box, 3000 of a tile's 2800 with pages of 16), 6 issues the
+// MMAs, 7 and 8 copy Q.  S and P are double-buffered, so S of the next tile and O of the last run
 // beside the softmax; a unit's output is written after the next unit's first softmax.
 #pragma once
 #include <cuda.h>
@@ -52,9 +53,9 @@ using vplan::kTileKeys;
 constexpr int kMaxB = 4096;
 constexpr int kMaxCtas = 160;                     // grid: one CTA per SM, at most this many
 constexpr int kMaxRows = 128;                     // rows of a query tile
-constexpr int kThreads = 256;
+constexpr int kThreads = 288;
 constexpr int kSoftThreads = 128;
-constexpr int kWarpLoad = 4, kWarpMma = 5, kWarpQ = 6;
+constexpr int kWarpK = 4, kWarpV = 5, kWarpMma = 6, kWarpQ = 7;
 constexpr int kQThreads = 64;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWaitHintNs = 20000;
@@ -112,6 +113,7 @@ struct Cfg {
 };
 
 constexpr int kMaxStages = 10;
+constexpr int kMaxBoxes = kTileKeys / 16;         // pages of a tile at most
 
 struct Ctl {
     unsigned long long kv_full[kMaxStages], kv_empty[kMaxStages];
@@ -281,6 +283,13 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi)
 {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -432,60 +441,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk w;
     bool more = w.begin(p, t1 > t0 ? ctl.start_b : 0, t1 > t0 ? ctl.start_off : 0, t1 - t0);
 
-    if (warp == kWarpLoad) {
-        // ---------------------------------------------------- K and V pages into the ring
+    if (warp == kWarpK || warp == kWarpV) {
+        // ---------------------------------------------------- K or V pages into the ring
         const int boxes = kTileKeys / p.ps;       // pages of a tile
-        uint32_t issued = 0;
+        const void *map = warp == kWarpK ? &tm_k : &tm_v;
+        const uint32_t first = warp == kWarpK ? 0 : 1;
+        uint32_t i = 0;                           // K of tile i is the ring's copy 2 i, V 2 i + 1
         bool ok = true;
-        // page ids one tile ahead of the copies
-        auto page_of = [&](int kt, int keys) {
-            const int key = kt * kTileKeys + lane * p.ps;
-            if (lane >= boxes || key >= keys) return -1;
-            int page = p.pages[static_cast<size_t>(w.b) * p.max_pages + key / p.ps];
-            if (page < 0 || page >= p.num_pages) {
-                record_error(DSPARK_INVALID_PAGE);
-                page = 0;
-            }
-            return page;
+        // lane j: page j of the tile, -1 behind the last key; read one tile ahead of the copies
+        auto live_at = [&](int kt) {
+            return max(min(boxes, (w.keys(p) - kt * kTileKeys - 1) / p.ps + 1), 0);
         };
-        int kt = w.kt;
-        int page = more ? page_of(kt, w.keys(p)) : -1;
-        while (more && ok) {
-            const int h = w.h, cur = page;
-            if (++kt < w.kt_end) {
-                page = page_of(kt, w.keys(p));
-            } else {
+        auto page_at = [&](int kt, int live) {
+            return lane < live ? __ldg(p.pages + static_cast<size_t>(w.b) * p.max_pages +
+                                       kt * boxes + lane)
+                               : 0;
+        };
+        int kt = w.kt, live = 0, page = 0;
+        if (more) {
+            live = live_at(kt);
+            page = page_at(kt, live);
+        }
+        while (more) {
+            const int h = w.h, n = live;
+            int cur = page;
+            if (++kt == w.kt_end) {
                 more = w.next(p);
                 kt = w.kt;
-                page = more ? page_of(kt, w.keys(p)) : -1;
             }
-            const int live = __popc(__ballot_sync(0xFFFFFFFFu, cur >= 0));
+            if (more) {
+                live = live_at(kt);
+                page = page_at(kt, live);
+            }
+            if (cur < 0 || cur >= p.num_pages) {
+                record_error(DSPARK_INVALID_PAGE);
+                cur = 0;
+            }
+            cur = (cur * p.Hkv + h) * p.ps;       // the page's first row of the cache
+            const uint32_t slot = (2 * i + first) % C::kStages, use = (2 * i + first) / C::kStages;
+            ok = warp_wait(kv_empty + 8 * slot, (use & 1u) ^ 1u, ctl, p);
+            if (!ok) break;
+            int row[kMaxBoxes];
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const uint32_t slot = issued % C::kStages;
-                const uint32_t parity = ((issued / C::kStages) & 1u) ^ 1u;
-                if (!warp_wait(kv_empty + 8 * slot, parity, ctl, p)) {
-                    ok = false;
-                    break;
-                }
-                __syncwarp();
+            for (int j = 0; j < kMaxBoxes; ++j) row[j] = __shfl_sync(0xFFFFFFFFu, cur, j);
+            if (elect_one()) {
                 const uint32_t bar = kv_full + 8 * slot;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(live) * p.ps * D * 2);
-                __syncwarp();
-                if (cur >= 0) {
-                    const uint32_t dst = s0 + C::kRing + slot * C::kTileBytes + lane * p.ps * 128;
-                    const int row = (cur * p.Hkv + h) * p.ps;
-                    const void *map = kv ? &tm_v : &tm_k;
-                    tma_load_2d_plain(dst, map, bar, 0, row);
-                    if (D == 128) tma_load_2d_plain(dst + C::kHalfBytes, map, bar, 64, row);
-                }
-                ++issued;
+                uint32_t dst = s0 + C::kRing + slot * C::kTileBytes;
+                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n) * p.ps * D * 2);
+#pragma unroll
+                for (int j = 0; j < kMaxBoxes; ++j)
+                    if (j < n) {
+                        tma_load_2d_plain(dst, map, bar, 0, row[j]);
+                        if (D == 128)
+                            tma_load_2d_plain(dst + C::kHalfBytes, map, bar, 64, row[j]);
+                        dst += p.ps * 128;
+                    }
             }
+            __syncwarp();
+            ++i;
         }
-        for (uint32_t s = 0; s < C::kStages; ++s) {   // copies land before the CTA ends
-            const uint32_t uses = issued / C::kStages + (s < issued % C::kStages ? 1 : 0);
-            if (uses > 0) wait_drain(kv_full + 8 * s, (uses - 1) & 1u, p);
+        // copies land before the CTA ends: this warp's among the ring's last
+        for (uint32_t t = i; t-- > 0;) {
+            const uint32_t c = 2 * t + first;
+            if (c + C::kStages <= 2 * i - 1) break;
+            wait_drain(kv_full + 8 * (c % C::kStages), (c / C::kStages) & 1u, p);
         }
     } else if (warp == kWarpMma) {
         // ---------------------------------------------------- S^T = K Q^T, O^T += V^T P
@@ -508,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!warp_wait(p_full + 8 * (j & 1), (j >> 1) & 1u, ctl, p))
                 return false;
             tc_fence_after();
-            if (lane == 0) {
+            if (elect_one()) {
                 const uint64_t a = smem_desc(s0 + C::kRing + slot * C::kTileBytes, C::kHalfBytes,
                                              1024, kSwizzle128B);
                 const uint64_t b = smem_desc(s0 + C::kP + pb * C::kPBytes, kTileKeys * 128, 1024,
@@ -539,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           p);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint64_t a = smem_desc(s0 + C::kRing + slot * C::kTileBytes, 16, 1024,
                                                  kSwizzle128B);
                     const uint64_t b = smem_desc(s0 + C::kQ + qb * C::kQBytes, 16, 1024,
@@ -565,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && i > 0) values(prev, i - 1);
         if (any) {                                // MMAs finish before the CTA ends
-            if (lane == 0) umma_commit(drain);
+            if (elect_one()) umma_commit(drain);
             __syncwarp();
             wait_drain(drain, 0, p);
         }
@@ -581,16 +600,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t dst = s0 + C::kQ + qb * C::kQBytes;
             const size_t row0 = static_cast<size_t>(w.start + w.first_token(p)) * p.Hq +
                                 static_cast<size_t>(w.h) * p.group;
-            for (int c = t; c < n * (D / 8); c += kQThreads) {
-                const int r = c / (D / 8), u = c % (D / 8);
+            constexpr int kStep = kQThreads / (D / 8);   // rows between a thread's
+            const int u = t % (D / 8);
+            int i = t / (D / 8) / p.group, g = t / (D / 8) - i * p.group;
+            for (int r = t / (D / 8); r < n; r += kStep) {
                 const uint32_t to = dst + (u >> 3) * (kN * 128) + r * 128 +
                                     (((u & 7) ^ (r & 7)) << 4);
-                if (r < rows) {
-                    const size_t row = row0 + static_cast<size_t>(r / p.group) * p.Hq + r % p.group;
-                    cp_async_16(to, p.q + row * D + u * 8);
-                } else {
+                if (r < rows)
+                    cp_async_16(to, p.q + (row0 + static_cast<size_t>(i) * p.Hq + g) * D + u * 8);
+                else
                     sts128(to, 0, 0, 0, 0);
-                }
+                for (g += kStep; g >= p.group; g -= p.group) ++i;
             }
             cp_async_wait_all();
             fence_proxy_async_smem();
@@ -630,22 +650,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool direct = s.starts && s.ends;
             const int part = 2 * blockIdx.x + (s.starts ? 1 : 0);
             const bool odd = *reinterpret_cast<volatile int *>(&ctl.odd[seg & 1]);
-            for (int c0 = 0; c0 < s.rows; c0 += 16) {
-                uint32_t o[16], l[16];
-                tmem_ld_32x32b_x16(lane_base + C::kColO + ob * kN + c0, o);
+            // a thread per row: 1 / l and the row's place in the output, or (m, l)
+            for (int c0 = 16 * warp; c0 < s.rows; c0 += 64) {
+                uint32_t l[16];
                 tmem_ld_32x32b_x16(lane_base + C::kColL + ob * kN + c0, l);
-                tmem_wait_ld16(o);
                 tmem_wait_ld16(l);
-                float v[16];
+                if (lane == 0)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    l[j] = __shfl_sync(0xFFFFFFFFu, l[j], 0);
-                    v[j] = __uint_as_float(o[j]);
-                    if (direct) v[j] *= 1.0f / __uint_as_float(l[j]);
+                    for (int j = 0; j < 16; ++j) red[c0 + j] = __uint_as_float(l[j]);
+            }
+            soft_sync();
+            if (tid < s.rows) {
+                const float l = red[tid];
+                if (direct) {
+                    const int i = tid / p.group;
+                    red[kN + tid] = __int_as_float(i * p.Hq + tid - i * p.group);
+                    red[tid] = 1.0f / l;
+                } else {
+                    p.part_ml[static_cast<size_t>(part) * kMaxRows + tid] =
+                        make_float2(m_s[(seg & 1) * kN + tid], l);
                 }
+            }
+            soft_sync();
+            const size_t row0 = static_cast<size_t>(s.row0) * p.Hq + static_cast<size_t>(s.h) * p.group;
+            for (int c0 = 0; c0 < s.rows; c0 += 16) {
+                uint32_t o[16];
+                float v[16];
+                tmem_ld_32x32b_x16(lane_base + C::kColO + ob * kN + c0, o);
+                tmem_wait_ld16(o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    v[j] = __uint_as_float(o[j]) * (direct ? red[c0 + j] : 1.0f);
                 if (odd && has_d) {               // values that are not finite, to who sees them
-                    for (int j = max(s.kt * kTileKeys, s.hidden); j < min(s.kt_end * kTileKeys, s.keys);
-                         ++j) {
+                    for (int j = max(s.kt * kTileKeys, s.hidden);
+                         j < min(s.kt_end * kTileKeys, s.keys); ++j) {
                         int page = p.pages[static_cast<size_t>(s.b) * p.max_pages + j / p.ps];
                         if (page < 0 || page >= p.num_pages) page = 0;
                         const uint32_t x =
@@ -662,32 +700,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (direct) {
                     // neighbouring lanes hold neighbouring channels: the even lane stores row
                     // j's pair, the odd lane row j + 1's
+                    const bool up = lane & 1;
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
-                        const bool up = lane & 1;
-                        const float got =
-                            __shfl_xor_sync(0xFFFFFFFFu, up ? v[j] : v[j + 1], 1);
+                        const float got = __shfl_xor_sync(0xFFFFFFFFu, up ? v[j] : v[j + 1], 1);
                         const uint32_t word =
                             up ? pack2_bf16(got, v[j + 1]) : pack2_bf16(v[j], got);
                         const int r = c0 + j + (up ? 1 : 0);
-                        if (r < s.rows && has_d) {
-                            const size_t row = static_cast<size_t>(s.row0 + r / p.group) * p.Hq +
-                                               static_cast<size_t>(s.h) * p.group + r % p.group;
-                            *reinterpret_cast<uint32_t *>(p.out + row * D + (d & ~1)) = word;
-                        }
+                        if (r < s.rows && has_d)
+                            *reinterpret_cast<uint32_t *>(
+                                p.out + (row0 + __float_as_int(red[kN + r])) * D + (d & ~1)) = word;
                     }
-                } else {
+                } else if (has_d) {
                     float *to = p.part_o + (static_cast<size_t>(part) * kMaxRows + c0) * D + d;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (c0 + j >= s.rows) break;
-                        if (has_d) to[j * D] = v[j];
-                        if (tid == 0)
-                            p.part_ml[static_cast<size_t>(part) * kMaxRows + c0 + j] =
-                                make_float2(m_s[(seg & 1) * kN + c0 + j], __uint_as_float(l[j]));
-                    }
+                    for (int j = 0; j < 16; ++j)
+                        if (c0 + j < s.rows) to[j * D] = v[j];
                 }
             }
+            soft_sync();                          // red is free again
             tc_fence_before();
             mbar_arrive(o_empty + 8 * ob);
         };
@@ -792,24 +823,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float t[16];
                         tmem_ld_32x32b_x16(col + c0, r);
                         const float4 *m4 = reinterpret_cast<const float4 *>(m_row + c0);
-                        float m[16];
+                        float4 m[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) m[q] = m4[q];
+                        tmem_wait_ld16(r);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const float4 x = m4[q];
-                            m[4 * q] = x.x, m[4 * q + 1] = x.y, m[4 * q + 2] = x.z,
-                                  m[4 * q + 3] = x.w;
+                            t[4 * q] = fmaf(__uint_as_float(r[4 * q]), sl, -m[q].x);
+                            t[4 * q + 1] = fmaf(__uint_as_float(r[4 * q + 1]), sl, -m[q].y);
+                            t[4 * q + 2] = fmaf(__uint_as_float(r[4 * q + 2]), sl, -m[q].z);
+                            t[4 * q + 3] = fmaf(__uint_as_float(r[4 * q + 3]), sl, -m[q].w);
                         }
-                        tmem_wait_ld16(r);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (c0 + j < from) t[j] = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) top = max3(top, t[j], t[j + 1]);
                         uint32_t word[8];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            t[j] = fmaf(__uint_as_float(r[j]), sl, -m[j]);
-                            if (c0 + j < from) t[j] = -INFINITY;
-                            top = fmaxf(top, t[j]);
-                            t[j] = exp2_approx(t[j]);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) word[j] = pack2_bf16(t[2 * j], t[2 * j + 1]);
+                        for (int j = 0; j < 8; ++j)
+                            word[j] = pack2_bf16(exp2_approx(t[2 * j]), exp2_approx(t[2 * j + 1]));
                         const uint32_t to = prow + (c0 >> 6) * (kTileKeys * 128);
                         const int u = (c0 >> 3) & 7;
                         sts128(to + ((u ^ (tid & 7)) << 4), word[0], word[1], word[2], word[3]);
