@@ -796,7 +796,7 @@ int dspark_verify_attention(const void *q, const void *k_cache, const void *v_ca
         !aligned(pages, 4) || !aligned(context, 4) || !aligned(row_start, 4) ||
         !aligned(workspace, 256) || !std::isfinite(scale))
         return DSPARK_INVALID_ARG;
-    if ((D != 64 && D != 128) || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 128 ||
+    if ((D != 64 && D != 128) || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > A::kMaxRows ||
         (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) || B < 1 ||
         B > A::kMaxB || row_capacity < 1 || max_pages < 1 || num_pages < 1 ||
         static_cast<long long>(B) * max_pages > INT32_MAX ||
@@ -847,14 +847,14 @@ int dspark_verify_attention(const void *q, const void *k_cache, const void *v_ca
     prm.part_o = reinterpret_cast<float *>(ws + lay.o);
     prm.timeout_ns = g_timeout_ns.load();
     // query tiles of 64 rows where a request's share of the row capacity (its gamma + 1 tokens,
-    // when the batch layout made it) fits one, else of 128
+    // when the batch layout made it) fits one, else of 112
     const bool wide = static_cast<long long>((row_capacity - 1) / B + 1) * prm.group > 64;
-    prm.tokens = (wide ? 128 : 64) / prm.group;
+    prm.tokens = (wide ? A::kMaxRows : 64) / prm.group;
     void (*kern)(const CUtensorMap, const CUtensorMap, const A::Params) =
-        D == 64 ? (wide ? A::verify_attention_kernel<64, 128> : A::verify_attention_kernel<64, 64>)
-                : (wide ? A::verify_attention_kernel<128, 128> : A::verify_attention_kernel<128, 64>);
-    const int smem = D == 64 ? (wide ? A::smem_bytes<64, 128>() : A::smem_bytes<64, 64>())
-                             : (wide ? A::smem_bytes<128, 128>() : A::smem_bytes<128, 64>());
+        D == 64 ? (wide ? A::verify_attention_kernel<64, A::kMaxRows> : A::verify_attention_kernel<64, 64>)
+                : (wide ? A::verify_attention_kernel<128, A::kMaxRows> : A::verify_attention_kernel<128, 64>);
+    const int smem = D == 64 ? (wide ? A::smem_bytes<64, A::kMaxRows>() : A::smem_bytes<64, 64>())
+                             : (wide ? A::smem_bytes<128, A::kMaxRows>() : A::smem_bytes<128, 64>());
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return DSPARK_CUDA_ERROR;
     const int grid = dev->sms < A::kMaxCtas ? dev->sms : A::kMaxCtas;

@@ -52,7 +52,7 @@ using vplan::kTileKeys;
 
 constexpr int kMaxB = 4096;
 constexpr int kMaxCtas = 160;                     // grid: one CTA per SM, at most this many
-constexpr int kMaxRows = 128;                     // rows of a query tile
+constexpr int kMaxRows = 112;                     // rows of a query tile
 constexpr int kThreads = 288;
 constexpr int kSoftThreads = 128;
 constexpr int kWarpK = 4, kWarpV = 5, kWarpMma = 6, kWarpQ = 7;
@@ -89,18 +89,18 @@ __host__ __device__ inline Layout workspace_layout(int D)
     return w;
 }
 
-// kN: rows of a query tile at most.  Two Q buffers, two O and l accumulators and five ring
-// tiles fit beside 64 rows; 128 rows leave room for one of each and four tiles.
+// kN: rows of a query tile at most.  Beside 64 rows fit five ring tiles of 32 KB and two
+// buffers of everything; beside 112, four tiles and one buffer of P and of O.
 template <int D, int kN>
 struct Cfg {
-    static constexpr int kQBufs = kN == 64 ? 2 : 1;
+    static constexpr int kQBufs = 2;
     static constexpr int kOBufs = kN == 64 ? 2 : 1;
     static constexpr int kPBufs = kN == 64 ? 2 : 1;
     static constexpr int kTileBytes = kTileKeys * D * 2;
     static constexpr int kHalfBytes = kTileKeys * 128;       // 64 channels of a tile
     static constexpr int kStages = (kN == 64 ? 5 : 4) * (128 / D);
     static constexpr int kQBytes = kN * D * 2;
-    static constexpr int kPBytes = kTileKeys * kN * 2;
+    static constexpr int kPBytes = (kN + 63) / 64 * kTileKeys * 128;
     static constexpr int kRing = 0;
     static constexpr int kQ = kRing + kStages * kTileBytes;
     static constexpr int kP = kQ + kQBufs * kQBytes;
@@ -119,7 +119,7 @@ struct Ctl {
     unsigned long long kv_full[kMaxStages], kv_empty[kMaxStages];
     unsigned long long s_full[2], p_full[2], p_free[2];
     unsigned long long q_full[2], q_empty[2], o_full[2], o_empty[2], drain;
-    long long start_off;                          // first tile's place in its request
+    long long start_off;                          // first place in its request
     unsigned long long sums[kThreads / 32];
     int start_b;
     uint32_t tmem;
@@ -210,14 +210,18 @@ struct Walk {
     {
         return vplan::Request{ctx, rows, p.tokens};
     }
-    __device__ __forceinline__ void segment(const Params &p)
+    // From place `at` of the unit on; false when the CTA's share ends before a key tile.
+    __device__ __forceinline__ bool segment(const Params &p, int at)
     {
         tiles = request(p).key_tiles(qt);
-        const long long n = min(static_cast<long long>(tiles - kt), left);
-        kt_end = kt + static_cast<int>(n);
+        const int n = static_cast<int>(
+            min(static_cast<long long>(vplan::kUnitCost + tiles - at), left));
         left -= n;
+        kt = max(at - vplan::kUnitCost, 0);
+        kt_end = at + n - vplan::kUnitCost;
+        return kt_end > kt;
     }
-    // The segment at tile `off` of request b0; false when there is none.
+    // The segment at place `off` of request b0; false when there is none.
     __device__ __forceinline__ bool begin(const Params &p, int b0, long long off, long long count)
     {
         left = count;
@@ -225,14 +229,13 @@ struct Walk {
         base = b0;
         load(p);
         take(b0);
-        place(request(p), off, h, qt, kt);
-        segment(p);
-        return true;
+        int at;
+        place(request(p), off, h, qt, at);
+        return segment(p, at);
     }
     __device__ __forceinline__ bool next(const Params &p)
     {
         if (left <= 0) return false;
-        kt = 0;
         if (++qt == request(p).query_tiles()) {
             qt = 0;
             if (++h == p.Hkv) {
@@ -248,8 +251,7 @@ struct Walk {
                 take(base + __ffs(more) - 1);
             }
         }
-        segment(p);
-        return true;
+        return segment(p, 0);
     }
     __device__ __forceinline__ int first_token(const Params &p) const { return qt * p.tokens; }
     // rows of the unit (tokens times query heads) and keys that it sees
@@ -415,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     before += sum - mine;
     const int G = vplan::ctas(T, gridDim.x);
     const int cta = blockIdx.x;
-    const long long t0 = cta < G ? vplan::first_tile(T, cta, G) : 0;
-    const long long t1 = cta < G ? vplan::first_tile(T, cta + 1, G) : 0;
+    const long long t0 = cta < G ? vplan::first_place(T, cta, G) : 0;
+    const long long t1 = cta < G ? vplan::first_place(T, cta + 1, G) : 0;
     if (t1 > t0 && before <= t0 && t0 < before + mine) {
         long long at = before;
         for (int r = r0; r < min(r0 + per, p.B); ++r) {
@@ -679,8 +681,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_32x32b_x16(lane_base + C::kColO + ob * kN + c0, o);
                 tmem_wait_ld16(o);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    v[j] = __uint_as_float(o[j]) * (direct ? red[c0 + j] : 1.0f);
+                for (int q = 0; q < 4; ++q) {
+                    float4 f = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                    if (direct) f = *reinterpret_cast<const float4 *>(red + c0 + 4 * q);
+                    v[4 * q] = __uint_as_float(o[4 * q]) * f.x;
+                    v[4 * q + 1] = __uint_as_float(o[4 * q + 1]) * f.y;
+                    v[4 * q + 2] = __uint_as_float(o[4 * q + 2]) * f.z;
+                    v[4 * q + 3] = __uint_as_float(o[4 * q + 3]) * f.w;
+                }
                 if (odd && has_d) {               // values that are not finite, to who sees them
                     for (int j = max(s.kt * kTileKeys, s.hidden);
                          j < min(s.kt_end * kTileKeys, s.keys); ++j) {
@@ -731,9 +739,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c0 + j < from) t[j] = -INFINITY;
             }
         };
-        // red[.][row] = the tile's maximum in each warp's keys
-        auto reduce = [&](uint32_t col, int n, int from) {
-            for (int c0 = 0; c0 < n; c0 += 16) {
+        // red[.][row] = the tile's maximum in each warp's keys; `share`: of a fourth of the rows
+        auto reduce = [&](uint32_t col, int n, int from, bool share) {
+            for (int c0 = share ? 16 * warp : 0; c0 < n; c0 += share ? 64 : 16) {
                 uint32_t r[16];
                 float t[16];
                 tmem_ld_32x32b_x16(col + c0, r);
@@ -775,38 +783,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                 await(s_full + 8 * (i & 1), (i >> 1) & 1u);
                 __syncwarp();
                 tc_fence_after();
-                if (kt == cur.kt) {               // m: the maximum over the first tile
-                    reduce(col, n, from);
+                const bool masked = (kt + 1) * kTileKeys > cur.hidden;
+                if (kt == cur.kt) {
+                    // m: the maximum over the first tile, or, where every row sees all of it,
+                    // over one warp's 32 keys, which does as well and takes a fourth of the time
+                    reduce(col, n, from, !masked);
                     soft_sync();
                     if (tid < n) {
-                        const float m = max_of(tid);
+                        const float m = masked ? max_of(tid) : red[((tid >> 4) & 3) * kN + tid];
                         m_row[tid] = m == -INFINITY ? 0.0f : m;
                     }
                     if (tid == 0) ctl.odd[seg & 1] = 0;
                     soft_sync();
                 }
-                if ((kt + 1) * kTileKeys > cur.hidden) {
+                if (masked) {
                     // values behind the last key, and those that are not finite
                     const uint32_t slot = (2 * i + 1) % C::kStages;
                     await(kv_full + 8 * slot, ((2 * i + 1) / C::kStages) & 1u);
-                    if (from > 0) {
-                        const uint32_t v = s0 + C::kRing + slot * C::kTileBytes + tid * 128;
+                    // 16-byte chunks in an order of the lane's own, so that neighbouring rows,
+                    // 128 bytes apart, meet different banks
+                    const uint32_t v = s0 + C::kRing + slot * C::kTileBytes + tid * 128;
+                    if (key >= cur.keys) {
+#pragma unroll
+                        for (int u = 0; u < D / 8; ++u)
+                            sts128(v + (u >> 3) * C::kHalfBytes + (((u ^ tid) & 7) << 4), 0, 0, 0, 0);
+                    } else if (from > 0) {
                         bool odd = false;
+#pragma unroll
                         for (int u = 0; u < D / 8; ++u) {
-                            const uint32_t at = v + (u >> 3) * C::kHalfBytes + ((u & 7) << 4);
-                            uint32_t x0 = 0, x1 = 0, x2 = 0, x3 = 0;
-                            if (key < cur.keys) {
-                                lds128(at, x0, x1, x2, x3);
-                                if (!not_finite(x0) && !not_finite(x1) && !not_finite(x2) &&
-                                    !not_finite(x3))
-                                    continue;
+                            const uint32_t at =
+                                v + (u >> 3) * C::kHalfBytes + (((u ^ tid) & 7) << 4);
+                            uint32_t x0, x1, x2, x3;
+                            lds128(at, x0, x1, x2, x3);
+                            if (not_finite(x0) || not_finite(x1) || not_finite(x2) ||
+                                not_finite(x3)) {
                                 odd = true;
-                                x0 = finite_or_zero(x0);
-                                x1 = finite_or_zero(x1);
-                                x2 = finite_or_zero(x2);
-                                x3 = finite_or_zero(x3);
+                                sts128(at, finite_or_zero(x0), finite_or_zero(x1),
+                                       finite_or_zero(x2), finite_or_zero(x3));
                             }
-                            sts128(at, x0, x1, x2, x3);
                         }
                         if (odd) *reinterpret_cast<volatile int *>(&ctl.odd[seg & 1]) = 1;
                     }
@@ -852,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 if (soft_any(weights() > kRaise)) {
                     // m rises: O and l of the tiles before are scaled, the weights made anew
-                    reduce(col, n, from);
+                    reduce(col, n, from, false);
                     soft_sync();
                     if (tid < n) {
                         const float old = m_row[tid], now = fmaxf(old, max_of(tid));

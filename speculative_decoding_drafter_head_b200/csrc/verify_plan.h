@@ -2,9 +2,10 @@
 //
 // A unit is (request, key head, query tile): up to `tokens` of the request's rows, all the
 // query heads of one key head, against the keys that the tile's last row sees, in key tiles
-// of 128.  All units' key tiles stand in one line (requests, then key heads, then query
-// tiles), and CTA c of G takes the tiles from floor(T c / G) to floor(T (c + 1) / G) of the
-// T: equal work whatever the lengths, a function of the lengths alone.  A unit cut by a
+// of 128.  All units stand in one line (requests, then key heads, then query tiles), each as
+// kUnitCost places, what starting and ending it costs in key tiles, and then one place a key
+// tile; CTA c of G takes the places from floor(T c / G) to floor(T (c + 1) / G) of the T: equal
+// work whatever the lengths, a function of the lengths alone.  A unit whose tiles are cut by a
 // border is joined from its parts.
 //
 // Plain integer arithmetic, the same on the host and the device.
@@ -20,6 +21,7 @@ namespace dspark {
 namespace vplan {
 
 constexpr int kTileKeys = 128;
+constexpr int kUnitCost = 3;
 
 // sum over i = 0 .. n - 1 of floor((a i + b) / 2^7), a, b >= 0, by Euclid's steps
 DSPARK_HD long long floor_sum(long long n, long long a, long long b)
@@ -56,7 +58,7 @@ struct Request {
         return ctx + static_cast<int>(end < rows ? end : rows);
     }
     DSPARK_HD int key_tiles(int qt) const { return (keys(qt) - 1) / kTileKeys + 1; }
-    // key tiles of query tiles 0 .. qt - 1, all but the last of which may be full
+    // places of query tiles 0 .. qt - 1, all but the last of which may be full
     DSPARK_HD long long before(int qt) const
     {
         if (qt <= 0) return 0;
@@ -65,23 +67,23 @@ struct Request {
                                                                kTileKeys - 1)
                                  : 0;
         if (full < qt) sum += key_tiles(full);
-        return sum;
+        return sum + static_cast<long long>(qt) * kUnitCost;
     }
     DSPARK_HD long long per_head() const { return before(query_tiles()); }
 };
 
-// first key tile of CTA c of G
-DSPARK_HD long long first_tile(long long T, int c, int G) { return T * c / G; }
-// the CTA that holds tile t
+// first place of CTA c of G
+DSPARK_HD long long first_place(long long T, int c, int G) { return T * c / G; }
+// the CTA that holds place t
 DSPARK_HD int cta_of(long long T, long long t, int G)
 {
     return static_cast<int>(((t + 1) * G - 1) / T);
 }
-// CTAs that take part: each has at least one tile
+// CTAs that take part: each has at least one place
 DSPARK_HD int ctas(long long T, int most) { return T < most ? static_cast<int>(T) : most; }
 
-// Place of tile `at` of a request with per_head() * heads tiles: key head, query tile, key tile.
-DSPARK_HD void place(const Request &r, long long at, int &h, int &qt, int &kt)
+// Place `at` of a request with per_head() * heads places: key head, query tile, place in the unit.
+DSPARK_HD void place(const Request &r, long long at, int &h, int &qt, int &in_unit)
 {
     const long long per = r.per_head();
     h = static_cast<int>(at / per);
@@ -93,7 +95,7 @@ DSPARK_HD void place(const Request &r, long long at, int &h, int &qt, int &kt)
         else hi = mid - 1;
     }
     qt = lo;
-    kt = static_cast<int>(rest - r.before(lo));
+    in_unit = static_cast<int>(rest - r.before(lo));
 }
 
 }  // namespace vplan

@@ -349,8 +349,8 @@ CASES = [
     ([-1, -1], [0, 0], 4, 4, 64, 16),                       # nothing at all
     ([1000, 3, 77], [17, 9, 1], 32, 8, 128, 16),            # 68 rows to a key head
     ([513], [25], 64, 8, 128, 64),                          # 200 rows to a key head
-    ([63, 260], [7, 8], 128, 1, 128, 32),                   # every token a tile of rows
-    ([33, 1029], [5, 3], 127, 1, 64, 16),                   # an odd group that fills no tile
+    ([63, 260], [7, 8], 112, 1, 128, 32),                   # every token a tile of rows
+    ([33, 1029], [5, 3], 111, 1, 64, 16),                   # an odd group that fills no tile
     ([0], [300], 4, 2, 64, 16),                             # a prompt
     ([200], [129], 7, 1, 128, 128),                         # a piece of a prompt
     ([20011], [4], 12, 4, 128, 16),                         # one long request

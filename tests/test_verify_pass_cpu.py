@@ -75,7 +75,7 @@ def attention(**kw):
     (dict(out=HALF), INVALID), (dict(vc=HALF), INVALID), (dict(ws=HALF), INVALID),
     (dict(pages=ODD), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(D=96), SHAPE), (dict(Hkv=0), SHAPE),
-    (dict(Hq=12), SHAPE), (dict(Hq=4), SHAPE), (dict(Hq=129, Hkv=1), SHAPE), (dict(ps=8), SHAPE),
+    (dict(Hq=12), SHAPE), (dict(Hq=4), SHAPE), (dict(Hq=113, Hkv=1), SHAPE), (dict(ps=8), SHAPE),
     (dict(ps=24), SHAPE), (dict(ps=256), SHAPE), (dict(B=0), SHAPE), (dict(B=4097), SHAPE),
     (dict(cap=0), SHAPE), (dict(max_pages=0), SHAPE), (dict(num_pages=0), SHAPE),
     (dict(num_pages=1 << 25), SHAPE), (dict(max_pages=1 << 30), SHAPE), (dict(wsb=16), SMALL),
