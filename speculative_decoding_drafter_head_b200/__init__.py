@@ -248,18 +248,36 @@ def verify_prefix(x, L, target, accepted_out, bonus_out, stream=None):
     _check("dspark_verify_prefix", st)
 
 
-def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _ptr(t, name, dtype, shape, device):
+    """The address of a tensor that a call of the verification pass can take as it is, else the
+    error that says why not.  One pass step makes these calls for every layer, so the checks
+    are few and cheap: 0.4 us a tensor."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous() and
+                t.get_device() == device):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
-def _one_device(**tensors):
-    """The library launches on the current device: every tensor must be there."""
+def _dims(t, n, name):
+    if getattr(t, "ndim", None) != n:
+        raise ValueError(f"{name} must be a tensor of {n} dimensions")
+    return t.shape
+
+
+def _here(stream):
+    """Current device, and the raw stream to launch on."""
     import torch
-    here = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.is_cuda and t.device.index != here:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+    torch.cuda._lazy_init()
+    device = torch._C._cuda_getDevice()
+    if stream is None:
+        return device, torch._C._cuda_getCurrentRawStream(device)
+    return device, stream.cuda_stream
 
 
 def verify_layout(L, context, rows, pages, held, free_pages, free_count, row_start, position, slot,
@@ -271,33 +289,31 @@ def verify_layout(L, context, rows, pages, held, free_pages, free_count, row_sta
     free_count [1]; row_start [B + 1]; position, slot, token [row_capacity]; anchor [B],
     x [B, gamma]: all int32.  L, context, rows, pages, held, free_pages and free_count are
     the cache's state, updated in place."""
-    import torch
-    i32 = torch.int32
-    B, max_pages = pages.shape
-    cap = position.numel()
+    from torch import int32 as i32
+    B, max_pages = _dims(pages, 2, "pages")
+    cap, = _dims(position, 1, "position")
+    num_pages, = _dims(free_pages, 1, "free_pages")
     if (anchor is None) != (token is None) or (x is None) != (token is None):
         raise ValueError("anchor, x and token go together")
-    args = dict(L=L, anchor=anchor, x=x, accepted=accepted, context=context, rows=rows, pages=pages,
-                held=held, free_pages=free_pages, free_count=free_count, row_start=row_start,
-                position=position, slot=slot, token=token)
-    ptr = {k: None if t is None else _dev(t, i32, k) for k, t in args.items()}
-    _one_device(**args)
-    for name in ("L", "context", "rows", "held", "anchor", "accepted"):
-        if args[name] is not None:
-            _shape(args[name], (B,), name)
-    _shape(row_start, (B + 1,), "row_start")
-    _shape(free_count, (1,), "free_count")
-    for name in ("position", "slot", "token"):
-        if args[name] is not None:
-            _shape(args[name], (cap,), name)
-    if x is not None:
-        _shape(x, (B, gamma), "x")
+    for name, t in (("L", L), ("context", context)):
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+    dev, raw = _here(stream)
+    per = (B,)
     st = load().dspark_verify_layout(
-        ptr["L"], ptr["anchor"], ptr["x"], ptr["accepted"], ptr["context"], ptr["rows"],
-        ptr["pages"], ptr["held"], ptr["free_pages"], ptr["free_count"], B, int(gamma),
-        int(page_size), max_pages, free_pages.numel(), cap, ptr["row_start"], ptr["position"],
-        ptr["slot"], ptr["token"], _stream(stream))
-    _check("dspark_verify_layout", st)
+        _ptr(L, "L", i32, per, dev),
+        None if token is None else _ptr(anchor, "anchor", i32, per, dev),
+        None if token is None else _ptr(x, "x", i32, (B, gamma), dev),
+        None if accepted is None else _ptr(accepted, "accepted", i32, per, dev),
+        _ptr(context, "context", i32, per, dev), _ptr(rows, "rows", i32, per, dev),
+        _ptr(pages, "pages", i32, (B, max_pages), dev), _ptr(held, "held", i32, per, dev),
+        _ptr(free_pages, "free_pages", i32, (num_pages,), dev),
+        _ptr(free_count, "free_count", i32, (1,), dev), B, gamma, page_size, max_pages, num_pages,
+        cap, _ptr(row_start, "row_start", i32, (B + 1,), dev),
+        _ptr(position, "position", i32, (cap,), dev), _ptr(slot, "slot", i32, (cap,), dev),
+        None if token is None else _ptr(token, "token", i32, (cap,), dev), raw)
+    if st:
+        _check("dspark_verify_layout", st)
 
 
 def qk_norm_rope_store(qkv, position, slot, n_rows, q_out, k_cache, v_cache, q_weight=None,
@@ -309,39 +325,29 @@ def qk_norm_rope_store(qkv, position, slot, n_rows, q_out, k_cache, v_cache, q_w
     qkv [row_capacity, (Hq + 2 Hkv) D] bf16, rows may be strided; position, slot
     [row_capacity] int32; n_rows [1] int32; q_out [row_capacity, Hq, D]; caches [num_pages,
     Hkv, page_size, D]; weights [D] bf16; inv_freq [rot_dim / 2] fp32."""
-    import torch
-    bf = torch.bfloat16
-    cap, Hq, D = q_out.shape
-    num_pages, Hkv, page_size, _ = k_cache.shape
-    if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda or qkv.dtype != bf:
+    from torch import bfloat16 as bf, float32 as f32, int32 as i32
+    cap, Hq, D = _dims(q_out, 3, "q_out")
+    num_pages, Hkv, page_size, _ = _dims(k_cache, 4, "k_cache")
+    _dims(qkv, 2, "qkv")
+    if not qkv.is_cuda or qkv.dtype is not bf:
         raise TypeError("qkv must be a CUDA tensor of torch.bfloat16")
-    _shape(qkv, (cap, (Hq + 2 * Hkv) * D), "qkv")
-    if qkv.stride(1) != 1:
-        raise ValueError("qkv must be contiguous along its channels")
-    stride = qkv.stride(0) if cap > 1 else qkv.shape[1]
-    _shape(k_cache, (num_pages, Hkv, page_size, D), "k_cache")
-    _shape(v_cache, k_cache.shape, "v_cache")
-    _shape(position, (cap,), "position")
-    _shape(slot, (cap,), "slot")
-    _shape(n_rows, (1,), "n_rows")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _shape(w, (D,), name)
-    if inv_freq is not None and inv_freq.dim() != 1:
-        raise ValueError("inv_freq must have one dimension")
-    _one_device(qkv=qkv, position=position, slot=slot, n_rows=n_rows, q_out=q_out, k_cache=k_cache,
-                v_cache=v_cache, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq)
+    dev, raw = _here(stream)
+    width = (Hq + 2 * Hkv) * D
+    if qkv.shape != (cap, width) or qkv.stride(1) != 1 or qkv.get_device() != dev:
+        raise ValueError(f"qkv must be [{cap}, {width}] on cuda:{dev}, contiguous along its channels")
+    cache, w = (num_pages, Hkv, page_size, D), (D,)
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
     st = load().dspark_qk_norm_rope_store(
-        C.c_void_p(qkv.data_ptr()), stride,
-        None if q_weight is None else _dev(q_weight, bf, "q_weight"),
-        None if k_weight is None else _dev(k_weight, bf, "k_weight"), float(eps),
-        None if inv_freq is None else _dev(inv_freq, torch.float32, "inv_freq"),
-        0 if inv_freq is None else 2 * inv_freq.numel(), int(bool(interleaved)), float(rope_scale),
-        _dev(position, torch.int32, "position"), _dev(slot, torch.int32, "slot"),
-        _dev(n_rows, torch.int32, "n_rows"), cap, Hq, Hkv, D, page_size, num_pages,
-        _dev(q_out, bf, "q_out"), _dev(k_cache, bf, "k_cache"), _dev(v_cache, bf, "v_cache"),
-        _stream(stream))
-    _check("dspark_qk_norm_rope_store", st)
+        qkv.data_ptr(), qkv.stride(0) if cap > 1 else width,
+        None if q_weight is None else _ptr(q_weight, "q_weight", bf, w, dev),
+        None if k_weight is None else _ptr(k_weight, "k_weight", bf, w, dev), eps,
+        None if inv_freq is None else _ptr(inv_freq, "inv_freq", f32, (rot // 2,), dev), rot,
+        1 if interleaved else 0, rope_scale, _ptr(position, "position", i32, (cap,), dev),
+        _ptr(slot, "slot", i32, (cap,), dev), _ptr(n_rows, "n_rows", i32, (1,), dev), cap, Hq, Hkv,
+        D, page_size, num_pages, _ptr(q_out, "q_out", bf, (cap, Hq, D), dev),
+        _ptr(k_cache, "k_cache", bf, cache, dev), _ptr(v_cache, "v_cache", bf, cache, dev), raw)
+    if st:
+        _check("dspark_qk_norm_rope_store", st)
 
 
 def verify_attention_workspace_bytes(Hq: int, Hkv: int, D: int) -> int:
@@ -355,25 +361,24 @@ def verify_attention(q, k_cache, v_cache, pages, context, row_start, out, worksp
 
     q, out [row_capacity, Hq, D]; caches [num_pages, Hkv, page_size, D] bf16; pages
     [B, max_pages], context [B], row_start [B + 1] int32.  scale defaults to D ** -0.5."""
-    import torch
-    bf, i32 = torch.bfloat16, torch.int32
-    cap, Hq, D = q.shape
-    num_pages, Hkv, page_size, _ = k_cache.shape
-    B, max_pages = pages.shape
-    _shape(k_cache, (num_pages, Hkv, page_size, D), "k_cache")
-    _shape(v_cache, k_cache.shape, "v_cache")
-    _shape(context, (B,), "context")
-    _shape(row_start, (B + 1,), "row_start")
-    _shape(out, q.shape, "out")
-    _one_device(q=q, k_cache=k_cache, v_cache=v_cache, pages=pages, context=context,
-                row_start=row_start, out=out, workspace=workspace)
+    from torch import bfloat16 as bf, int32 as i32, uint8
+    cap, Hq, D = _dims(q, 3, "q")
+    num_pages, Hkv, page_size, _ = _dims(k_cache, 4, "k_cache")
+    B, max_pages = _dims(pages, 2, "pages")
+    size, = _dims(workspace, 1, "workspace")
+    if not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    dev, raw = _here(stream)
+    rows, cache = (cap, Hq, D), (num_pages, Hkv, page_size, D)
     st = load().dspark_verify_attention(
-        _dev(q, bf, "q"), _dev(k_cache, bf, "k_cache"), _dev(v_cache, bf, "v_cache"),
-        _dev(pages, i32, "pages"), _dev(context, i32, "context"),
-        _dev(row_start, i32, "row_start"), B, cap, Hq, Hkv, D, page_size, max_pages, num_pages,
-        float(D ** -0.5 if scale is None else scale), _dev(out, bf, "out"),
-        _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream))
-    _check("dspark_verify_attention", st)
+        _ptr(q, "q", bf, rows, dev), _ptr(k_cache, "k_cache", bf, cache, dev),
+        _ptr(v_cache, "v_cache", bf, cache, dev), _ptr(pages, "pages", i32, (B, max_pages), dev),
+        _ptr(context, "context", i32, (B,), dev), _ptr(row_start, "row_start", i32, (B + 1,), dev),
+        B, cap, Hq, Hkv, D, page_size, max_pages, num_pages,
+        D ** -0.5 if scale is None else scale, _ptr(out, "out", bf, rows, dev),
+        _ptr(workspace, "workspace", uint8, (size,), dev), size, raw)
+    if st:
+        _check("dspark_verify_attention", st)
 
 
 def sts_fit_workspace_bytes(N: int, gamma: int, n_t: int, n_bins: int) -> int:

@@ -12,10 +12,14 @@
 // reduced to a fraction of a turn in fp64 before the fp32 sine and cosine: an fp32 product
 // would be off by 2^-24 m radians (0.06 at a position of a million).
 //
-// What bounds it: HBM, every channel read and written once.  A thread holds 8 channels (one
-// 16-byte load and store), so a head is D / 8 neighbouring lanes and its mean and its
-// rotation partners are shuffles.  The sines of a row are formed once per CTA, in shared
-// memory, and serve all its heads.
+// What bounds it: HBM, every channel read and written once; but 8 channels a lane leave room for
+// some 100 instructions only.  So a lane holds whole rotation pairs (4 channels from each half,
+// or 8 neighbours when interleaved) and needs no exchange for them, and the weights times
+// cosines and sines of its channels stay in registers for all heads of a row:
+//     y_a = inv (w_a c x_a - w_b s x_b),  y_b = inv (w_a s x_a + w_b c x_b)
+// (13000 rows of 48 heads of 128: 104 us with 16-byte chunks, shuffled partners and factors
+// from shared memory).  One warp takes a row, four units of two (D = 128) heads in flight; with
+// few rows the 8 warps of a CTA share one.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -27,7 +31,8 @@ namespace qknorm {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPairs = 64;                     // R / 2 <= 64
-constexpr int kMaxTile = 4;                       // rows per CTA
+constexpr int kBlocks = 3;                        // CTAs to an SM, at least
+constexpr int kInFlight = 2;                      // units a warp works on at once
 
 struct Params {
     const uint16_t *qkv;          // [rows][stride], heads Hq + Hkv + Hkv
@@ -38,7 +43,7 @@ struct Params {
     int rot, interleaved;
     float rope_scale;
     const int32_t *position, *slot, *n_rows;
-    int row_capacity, tile;       // rows per CTA
+    int row_capacity, share;      // warps that share a row: 1 or 8
     int Hq, Hkv, ps, num_pages;
     uint16_t *q_out, *k_cache, *v_cache;
 };
@@ -49,110 +54,147 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_store_kernel(const Params p)
+// Factors of a lane's four pairs for queries or keys: y_a = ac x_a - bs x_b, y_b = as x_a + bc x_b.
+struct Factors {
+    float ac[4], bs[4], as[4], bc[4];
+};
+
+template <int D, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_store_kernel(const Params p)
 {
     constexpr int kLanes = D / 8;                 // lanes of a head
-    constexpr int kHeadsPerWarp = 32 / kLanes;
-    __shared__ float2 turn[kMaxTile][kMaxPairs];  // (cos, sin) of the tile's rows
+    constexpr int kHeads = 32 / kLanes;           // heads of a unit
+    __shared__ float2 turn[kWarps][kMaxPairs];    // (cos, sin) of the CTA's rows
 
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n = min(max(*p.n_rows, 0), p.row_capacity);
-    const int row0 = blockIdx.x * p.tile;
-    const int rows = min(p.tile, n - row0);
+    const int per_cta = kWarps / p.share;
+    const int row0 = blockIdx.x * per_cta;
+    const int rows = min(per_cta, n - row0);
     if (rows <= 0) return;
     const int pairs = p.rot / 2;
     for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
         const int r = i / pairs, j = i - r * pairs;
-        // angle / pi in (-1, 1]: fraction of a turn, times two
+        // angle / pi in [-1, 1]: fraction of a turn, times two
         const double turns = static_cast<double>(p.position[row0 + r]) *
                              static_cast<double>(p.inv_freq[j]) * 0.15915494309189533577;
-        const float half = 2.0f * static_cast<float>(turns - rint(turns));
         float s, c;
-        sincospif(half, &s, &c);
+        sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &c);
         turn[r][j] = make_float2(c * p.rope_scale, s * p.rope_scale);
     }
     __syncthreads();
+    const int r = warp / p.share, row = row0 + r;
+    if (r >= rows) return;
 
-    const int lane = threadIdx.x & 31;
-    const int sub = lane % kLanes, ch = sub * 8;  // this lane's place in its head
+    // the lane's channels: ca .. ca + 3 and cb .. cb + 3; pair i is (a_i, b_i) of its factors
+    const int sub = lane % kLanes;
+    const bool halves = !kInterleaved && 8 * sub < p.rot;
+    const int ca = halves ? 4 * sub : 8 * sub, cb = halves ? pairs + 4 * sub : 8 * sub + 4;
+    const bool turns = 8 * sub < p.rot;
+    Factors fq, fk;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int xa = kInterleaved ? 8 * sub + 2 * i : ca + i;
+        const int xb = kInterleaved ? xa + 1 : cb + i;
+        float2 t = make_float2(1.0f, 0.0f);
+        if (turns) t = turn[r][kInterleaved ? xa / 2 : xa];
+        auto weight = [](const uint16_t *w, int ch) {
+            return w ? __uint_as_float(static_cast<uint32_t>(__ldg(w + ch)) << 16) : 1.0f;
+        };
+        const float qa = weight(p.q_weight, xa), qb = weight(p.q_weight, xb);
+        const float ka = weight(p.k_weight, xa), kb = weight(p.k_weight, xb);
+        fq.ac[i] = qa * t.x, fq.bs[i] = qb * t.y, fq.as[i] = qa * t.y, fq.bc[i] = qb * t.x;
+        fk.ac[i] = ka * t.x, fk.bs[i] = kb * t.y, fk.as[i] = ka * t.y, fk.bc[i] = kb * t.x;
+    }
+    const int slot = p.slot[row];
+    const int page = slot / p.ps;
+    const bool stored = slot >= 0 && page < p.num_pages;
+    if (!stored && lane == 0) record_error(DSPARK_INVALID_PAGE);
+    const size_t place =
+        stored ? (static_cast<size_t>(page) * p.Hkv * p.ps + (slot - page * p.ps)) * D : 0;
     const int heads = p.Hq + 2 * p.Hkv;
-    const int groups = (heads + kHeadsPerWarp - 1) / kHeadsPerWarp;
-    for (int u = threadIdx.x >> 5; u < rows * groups; u += kWarps) {
-        const int r = u / groups;
-        const int head = (u - r * groups) * kHeadsPerWarp + lane / kLanes;
-        const bool live = head < heads;
-        const int row = row0 + r;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live)
-            raw = __ldg(reinterpret_cast<const uint4 *>(p.qkv + row * p.stride +
-                                                        static_cast<long long>(head) * D + ch));
-        const bool is_q = head < p.Hq, is_v = head >= p.Hq + p.Hkv;
-        float y[8] = {bf16lo_to_f32(raw.x), bf16hi_to_f32(raw.x), bf16lo_to_f32(raw.y),
-                      bf16hi_to_f32(raw.y), bf16lo_to_f32(raw.z), bf16hi_to_f32(raw.z),
-                      bf16lo_to_f32(raw.w), bf16hi_to_f32(raw.w)};
-        // the mean and the partners of every lane, values included: shuffles need all lanes
-        float sq = 0.0f;
+    const int step = p.share * kHeads;            // heads from a warp's unit to its next
+    const uint16_t *from = p.qkv + row * p.stride + ca;
+    const int gap = cb - ca, first = (warp - r * p.share) * kHeads;
+
+    // the next units' channels are on their way while these are worked on
+    uint2 na[kInFlight], nb[kInFlight];
+    auto fetch = [&](int h0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sq = fmaf(y[i], y[i], sq);
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
-        const uint16_t *w = is_q ? p.q_weight : p.k_weight;
-        if (w && !is_v) {
-            const float inv = rsqrtf(sq * (1.0f / D) + p.eps);
-            const uint4 ww = __ldg(reinterpret_cast<const uint4 *>(w + ch));
-            const float wf[8] = {bf16lo_to_f32(ww.x), bf16hi_to_f32(ww.x), bf16lo_to_f32(ww.y),
-                                 bf16hi_to_f32(ww.y), bf16lo_to_f32(ww.z), bf16hi_to_f32(ww.z),
-                                 bf16lo_to_f32(ww.w), bf16hi_to_f32(ww.w)};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * wf[i];
-        }
-        if (p.rot) {
-            if (p.interleaved) {
-                if (!is_v && ch < p.rot) {
-#pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        const float2 t = turn[r][(ch + i) >> 1];
-                        const float a = y[i], b = y[i + 1];
-                        y[i] = a * t.x - b * t.y;
-                        y[i + 1] = a * t.y + b * t.x;
-                    }
-                }
-            } else {
-                // channels j and j + R/2 stand R/16 lanes apart
-                const bool low = ch < pairs;
-                const int from = low ? lane + pairs / 8 : lane - pairs / 8;
-                float o[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xFFFFFFFFu, y[i], from & 31);
-                if (!is_v && ch < p.rot) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 t = turn[r][low ? ch + i : ch + i - pairs];
-                        y[i] = low ? y[i] * t.x - o[i] * t.y : o[i] * t.y + y[i] * t.x;
-                    }
-                }
+        for (int f = 0; f < kInFlight; ++f) {
+            const int head = h0 + f * step + lane / kLanes;
+            na[f] = nb[f] = make_uint2(0, 0);
+            if (head < heads) {
+                const uint16_t *x = from + static_cast<size_t>(head) * D;
+                na[f] = __ldg(reinterpret_cast<const uint2 *>(x));
+                nb[f] = __ldg(reinterpret_cast<const uint2 *>(x + gap));
             }
         }
-        if (!live) continue;
-        const uint4 out = is_v ? raw
-                               : make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
-                                            pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-        if (is_q) {
-            *reinterpret_cast<uint4 *>(p.q_out + (static_cast<size_t>(row) * p.Hq + head) * D +
-                                       ch) = out;
-            continue;
+    };
+    fetch(first);
+    for (int u0 = first; u0 < heads; u0 += kInFlight * step) {
+        const int h0 = u0 + lane / kLanes;
+        uint2 xa[kInFlight], xb[kInFlight];
+#pragma unroll
+        for (int f = 0; f < kInFlight; ++f) xa[f] = na[f], xb[f] = nb[f];
+        fetch(u0 + kInFlight * step);
+#pragma unroll
+        for (int f = 0; f < kInFlight; ++f) {
+            const int head = h0 + f * step;
+            if (u0 + f * step >= heads) break;
+            float a[4] = {bf16lo_to_f32(xa[f].x), bf16hi_to_f32(xa[f].x), bf16lo_to_f32(xa[f].y),
+                          bf16hi_to_f32(xa[f].y)};
+            float b[4] = {bf16lo_to_f32(xb[f].x), bf16hi_to_f32(xb[f].x), bf16lo_to_f32(xb[f].y),
+                          bf16hi_to_f32(xb[f].y)};
+            float sq = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sq = fmaf(a[i], a[i], fmaf(b[i], b[i], sq));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
+            if (kInterleaved) {                   // neighbours are the pairs
+                const float t0 = a[1], t1 = a[3], t2 = b[0], t3 = b[2];
+                a[1] = a[2], a[2] = t2, a[3] = t3;
+                b[0] = t0, b[2] = b[1], b[1] = t1;
+            }
+            uint2 ya = xa[f], yb = xb[f];
+            // queries or keys; values stay as they are
+            auto turned = [&](const Factors &w, bool normed) {
+                const float inv = normed ? rsqrtf(sq * (1.0f / D) + p.eps) : 1.0f;
+                float u[4], v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (turns) {
+                        u[i] = inv * (w.ac[i] * a[i] - w.bs[i] * b[i]);
+                        v[i] = inv * (w.as[i] * a[i] + w.bc[i] * b[i]);
+                    } else {                      // no zero times infinity
+                        u[i] = inv * (w.ac[i] * a[i]);
+                        v[i] = inv * (w.bc[i] * b[i]);
+                    }
+                }
+                if (kInterleaved) {
+                    ya = make_uint2(pack_bf16(u[0], v[0]), pack_bf16(u[1], v[1]));
+                    yb = make_uint2(pack_bf16(u[2], v[2]), pack_bf16(u[3], v[3]));
+                } else {
+                    ya = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
+                    yb = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                }
+            };
+            uint16_t *to;
+            if (head < p.Hq) {
+                turned(fq, p.q_weight != nullptr);
+                to = p.q_out + (static_cast<size_t>(row) * p.Hq + head) * D;
+            } else {
+                const bool key = head < p.Hq + p.Hkv;
+                if (key) turned(fk, p.k_weight != nullptr);
+                to = (key ? p.k_cache : p.v_cache) + place +
+                     static_cast<size_t>(head - p.Hq - (key ? 0 : p.Hkv)) * p.ps * D;
+                if (!stored) continue;
+            }
+            if (head < heads) {
+                *reinterpret_cast<uint2 *>(to + ca) = ya;
+                *reinterpret_cast<uint2 *>(to + cb) = yb;
+            }
         }
-        const int slot = p.slot[row];
-        const int page = slot / p.ps;
-        if (slot < 0 || page >= p.num_pages) {
-            record_error(DSPARK_INVALID_PAGE);
-            continue;
-        }
-        const int h = head - p.Hq - (is_v ? p.Hkv : 0);
-        uint16_t *cache = is_v ? p.v_cache : p.k_cache;
-        *reinterpret_cast<uint4 *>(
-            cache + ((static_cast<size_t>(page) * p.Hkv + h) * p.ps + (slot - page * p.ps)) * D +
-            ch) = out;
     }
 }
 

@@ -32,10 +32,10 @@
 // border leave (m, l, O) in the workspace, and verify_join_kernel adds the parts up, in
 // order, so results do not depend on timing.  It is launched to overlap with this kernel's end.
 //
-// Warps: 0-3 softmax and output (thread = key of the tile, then channel of the output), 4 and
-// 5 copy K and V pages into a ring of 32 KB tiles by TMA (one box a page and 64 channels; one
-// warp for both took 90 cycles a box, 3000 of a tile's 2800 with pages of 16), 6 issues the
-// MMAs, 7 and 8 copy Q.  S and P are double-buffered, so S of the next tile and O of the last run
+// Warps: 0-7 softmax and output (two threads to a key of the tile, later to a channel of the
+// output, each with half of the rows), 8 and 9 copy K and V pages into a ring of 32 KB tiles by
+// TMA (one box a page and 64 channels; one warp for both took 90 cycles a box, 3000 of a
+// tile's 2800 with pages of 16), 10 issues the MMAs, 11 copies Q.  S and P are double-buffered, so S of the next tile and O of the last run
 // beside the softmax; a unit's output is written after the next unit's first softmax.
 #pragma once
 #include <cuda.h>
@@ -53,16 +53,15 @@ using vplan::kTileKeys;
 constexpr int kMaxB = 4096;
 constexpr int kMaxCtas = 160;                     // grid: one CTA per SM, at most this many
 constexpr int kMaxRows = 112;                     // rows of a query tile
-constexpr int kThreads = 288;
-constexpr int kSoftThreads = 128;
-constexpr int kWarpK = 4, kWarpV = 5, kWarpMma = 6, kWarpQ = 7;
-constexpr int kQThreads = 64;
+constexpr int kThreads = 384;
+constexpr int kSoftThreads = 256;
+constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpQ = 11;
+constexpr int kQThreads = 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWaitHintNs = 20000;
 constexpr float kRaise = 24.0f;                   // log2 of the weight at which m rises
 constexpr int kOnesBytes = 1152;                  // 8 x 2 core matrices of 128 B, one apart
-constexpr int kJoinThreads = 128;
-constexpr int kJoinSplit = 4;                     // CTAs that share a unit's rows
+constexpr int kJoinThreads = 512;
 
 struct Params {
     const uint16_t *q, *k_cache, *v_cache;
@@ -89,8 +88,9 @@ __host__ __device__ inline Layout workspace_layout(int D)
     return w;
 }
 
-// kN: rows of a query tile at most.  Beside 64 rows fit five ring tiles of 32 KB and two
-// buffers of everything; beside 112, four tiles and one buffer of P and of O.
+// kN: rows of a query tile at most.  Beside 64 rows fit four ring tiles of 32 KB and two
+// buffers of everything; beside 112, four tiles and one buffer of P and of O (a fifth tile
+// gains nothing).
 template <int D, int kN>
 struct Cfg {
     static constexpr int kQBufs = 2;
@@ -98,7 +98,7 @@ struct Cfg {
     static constexpr int kPBufs = kN == 64 ? 2 : 1;
     static constexpr int kTileBytes = kTileKeys * D * 2;
     static constexpr int kHalfBytes = kTileKeys * 128;       // 64 channels of a tile
-    static constexpr int kStages = (kN == 64 ? 5 : 4) * (128 / D);
+    static constexpr int kStages = 4 * (128 / D);
     static constexpr int kQBytes = kN * D * 2;
     static constexpr int kPBytes = (kN + 63) / 64 * kTileKeys * 128;
     static constexpr int kRing = 0;
@@ -112,7 +112,7 @@ struct Cfg {
     static_assert(kColL + kOBufs * kN <= kTmemCols, "tensor memory");
 };
 
-constexpr int kMaxStages = 10;
+constexpr int kMaxStages = 8;
 constexpr int kMaxBoxes = kTileKeys / 16;         // pages of a tile at most
 
 struct Ctl {
@@ -262,7 +262,7 @@ struct Walk {
     __device__ __forceinline__ int keys(const Params &p) const { return request(p).keys(qt); }
 };
 
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 2, 256;" ::: "memory"); }
 
 __device__ __forceinline__ bool soft_any(bool v)
 {
@@ -270,7 +270,7 @@ __device__ __forceinline__ bool soft_any(bool v)
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 2, 128, p;\n\t"
+        "bar.red.or.pred q, 2, 256, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(any)
         : "r"(static_cast<uint32_t>(v))
@@ -450,57 +450,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t first = warp == kWarpK ? 0 : 1;
         uint32_t i = 0;                           // K of tile i is the ring's copy 2 i, V 2 i + 1
         bool ok = true;
-        // lane j: page j of the tile, -1 behind the last key; read one tile ahead of the copies
-        auto live_at = [&](int kt) {
-            return max(min(boxes, (w.keys(p) - kt * kTileKeys - 1) / p.ps + 1), 0);
+        // A segment, and page ids 32 at a time, those after them and the next segment's first
+        // on their way meanwhile: a table's line comes from HBM, which is most of a tile's time.
+        struct Seg {
+            int b, h, kt, kt_end, pages;
         };
-        auto page_at = [&](int kt, int live) {
-            return lane < live ? __ldg(p.pages + static_cast<size_t>(w.b) * p.max_pages +
-                                       kt * boxes + lane)
-                               : 0;
+        auto segment = [&]() {
+            return Seg{w.b, w.h, w.kt, w.kt_end, (w.keys(p) - 1) / p.ps + 1};
         };
-        int kt = w.kt, live = 0, page = 0;
+        auto ids_at = [&](const Seg &s, int at) {
+            return at + lane < s.pages
+                       ? __ldg(p.pages + static_cast<size_t>(s.b) * p.max_pages + at + lane)
+                       : 0;
+        };
+        Seg nxt = {};
+        int nids = 0;
         if (more) {
-            live = live_at(kt);
-            page = page_at(kt, live);
+            nxt = segment();
+            nids = ids_at(nxt, nxt.kt * boxes);
         }
-        while (more) {
-            const int h = w.h, n = live;
-            int cur = page;
-            if (++kt == w.kt_end) {
-                more = w.next(p);
-                kt = w.kt;
-            }
+        while (more && ok) {
+            const Seg cur = nxt;
+            int base = cur.kt * boxes, ids = nids, ids2 = ids_at(cur, base + 32);
+            more = w.next(p);
             if (more) {
-                live = live_at(kt);
-                page = page_at(kt, live);
+                nxt = segment();
+                nids = ids_at(nxt, nxt.kt * boxes);
             }
-            if (cur < 0 || cur >= p.num_pages) {
-                record_error(DSPARK_INVALID_PAGE);
-                cur = 0;
-            }
-            cur = (cur * p.Hkv + h) * p.ps;       // the page's first row of the cache
-            const uint32_t slot = (2 * i + first) % C::kStages, use = (2 * i + first) / C::kStages;
-            ok = warp_wait(kv_empty + 8 * slot, (use & 1u) ^ 1u, ctl, p);
-            if (!ok) break;
-            int row[kMaxBoxes];
+            for (int kt = cur.kt; kt < cur.kt_end; ++kt) {
+                if (kt * boxes == base + 32) {
+                    base += 32;
+                    ids = ids2;
+                    ids2 = ids_at(cur, base + 32);
+                }
+                const int n = min(boxes, cur.pages - kt * boxes);   // live pages, the first ones
+                int id = __shfl_sync(0xFFFFFFFFu, ids, (kt * boxes - base + lane) & 31);
+                if (lane < n && (id < 0 || id >= p.num_pages)) {
+                    record_error(DSPARK_INVALID_PAGE);
+                    id = 0;
+                }
+                id = (id * p.Hkv + cur.h) * p.ps;   // the page's first row of the cache
+                int row[kMaxBoxes];
 #pragma unroll
-            for (int j = 0; j < kMaxBoxes; ++j) row[j] = __shfl_sync(0xFFFFFFFFu, cur, j);
-            if (elect_one()) {
-                const uint32_t bar = kv_full + 8 * slot;
-                uint32_t dst = s0 + C::kRing + slot * C::kTileBytes;
-                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n) * p.ps * D * 2);
+                for (int j = 0; j < kMaxBoxes; ++j) row[j] = __shfl_sync(0xFFFFFFFFu, id, j);
+                const uint32_t slot = (2 * i + first) % C::kStages;
+                ok = warp_wait(kv_empty + 8 * slot, (((2 * i + first) / C::kStages) & 1u) ^ 1u, ctl,
+                               p);
+                if (!ok) break;
+                if (elect_one()) {
+                    const uint32_t bar = kv_full + 8 * slot;
+                    uint32_t dst = s0 + C::kRing + slot * C::kTileBytes;
+                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n) * p.ps * D * 2);
 #pragma unroll
-                for (int j = 0; j < kMaxBoxes; ++j)
-                    if (j < n) {
-                        tma_load_2d_plain(dst, map, bar, 0, row[j]);
-                        if (D == 128)
-                            tma_load_2d_plain(dst + C::kHalfBytes, map, bar, 64, row[j]);
-                        dst += p.ps * 128;
-                    }
+                    for (int j = 0; j < kMaxBoxes; ++j)
+                        if (j < n) {
+                            tma_load_2d_plain(dst, map, bar, 0, row[j]);
+                            if (D == 128)
+                                tma_load_2d_plain(dst + C::kHalfBytes, map, bar, 64, row[j]);
+                            dst += p.ps * 128;
+                        }
+                }
+                __syncwarp();
+                ++i;
             }
-            __syncwarp();
-            ++i;
         }
         // copies land before the CTA ends: this warp's among the ring's last
         for (uint32_t t = i; t-- > 0;) {
@@ -624,9 +636,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------- softmax and output
         float *m_s = reinterpret_cast<float *>(smem + C::kM);
         float *red = reinterpret_cast<float *>(smem + C::kRed);
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        // warps w and w + 4 read the same 32 lanes, keys or channels, and take 8 or 16 rows in turn
+        const int quad = warp & 3, half = warp >> 2, at = tid & 127;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         // the output's channel of this thread (M = 64 puts 16 rows in each warp's lanes)
-        const int d = D == 128 ? tid : warp * 16 + (lane & 15);
+        const int d = D == 128 ? at : quad * 16 + (lane & 15);
         const bool has_d = D == 128 || lane < 16;
         const float sl = p.scale_log2;
         struct Seg {
@@ -653,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int part = 2 * blockIdx.x + (s.starts ? 1 : 0);
             const bool odd = *reinterpret_cast<volatile int *>(&ctl.odd[seg & 1]);
             // a thread per row: 1 / l and the row's place in the output, or (m, l)
-            for (int c0 = 16 * warp; c0 < s.rows; c0 += 64) {
+            for (int c0 = 16 * warp; c0 < s.rows; c0 += 128) {
                 uint32_t l[16];
                 tmem_ld_32x32b_x16(lane_base + C::kColL + ob * kN + c0, l);
                 tmem_wait_ld16(l);
@@ -675,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             soft_sync();
             const size_t row0 = static_cast<size_t>(s.row0) * p.Hq + static_cast<size_t>(s.h) * p.group;
-            for (int c0 = 0; c0 < s.rows; c0 += 16) {
+            for (int c0 = 16 * half; c0 < s.rows; c0 += 32) {
                 uint32_t o[16];
                 float v[16];
                 tmem_ld_32x32b_x16(lane_base + C::kColO + ob * kN + c0, o);
@@ -739,16 +753,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c0 + j < from) t[j] = -INFINITY;
             }
         };
-        // red[.][row] = the tile's maximum in each warp's keys; `share`: of a fourth of the rows
+        // red[q][row] = the tile's maximum in the keys of lanes 32 q on; `share`: rows 16 w on in
+        // warp w's keys alone
         auto reduce = [&](uint32_t col, int n, int from, bool share) {
-            for (int c0 = share ? 16 * warp : 0; c0 < n; c0 += share ? 64 : 16) {
+            for (int c0 = 16 * (share ? warp : half); c0 < n; c0 += share ? 128 : 32) {
                 uint32_t r[16];
                 float t[16];
                 tmem_ld_32x32b_x16(col + c0, r);
                 tmem_wait_ld16(r);
                 scores(r, t, c0, from);
                 const float m = column_max(t);
-                if ((lane & 1) == 0) red[warp * kN + c0 + (lane >> 1)] = m;
+                if ((lane & 1) == 0) red[quad * kN + c0 + (lane >> 1)] = m;
             }
         };
         auto max_of = [&](int r) {
@@ -775,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float *m_row = m_s + (seg & 1) * kN;
             for (int kt = cur.kt; kt < cur.kt_end; ++kt) {
                 const uint32_t col = lane_base + C::kColS + (i & 1) * kN;
-                const int key = kt * kTileKeys + tid;
+                const int key = kt * kTileKeys + at;
                 // rows from `from` on see this thread's key
                 int from = 0;
                 if (key >= cur.keys) from = kMaxRows;
@@ -786,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool masked = (kt + 1) * kTileKeys > cur.hidden;
                 if (kt == cur.kt) {
                     // m: the maximum over the first tile, or, where every row sees all of it,
-                    // over one warp's 32 keys, which does as well and takes a fourth of the time
+                    // over one warp's 32 keys, which does as well and is one exchange for a warp
                     reduce(col, n, from, !masked);
                     soft_sync();
                     if (tid < n) {
@@ -800,67 +815,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // values behind the last key, and those that are not finite
                     const uint32_t slot = (2 * i + 1) % C::kStages;
                     await(kv_full + 8 * slot, ((2 * i + 1) / C::kStages) & 1u);
-                    // 16-byte chunks in an order of the lane's own, so that neighbouring rows,
-                    // 128 bytes apart, meet different banks
-                    const uint32_t v = s0 + C::kRing + slot * C::kTileBytes + tid * 128;
+                    // 16-byte chunks, a half of the row each, in an order of the lane's own, so
+                    // that neighbouring rows, 128 bytes apart, meet different banks
+                    const uint32_t v = s0 + C::kRing + slot * C::kTileBytes + at * 128;
+                    auto chunk = [&](int e) {
+                        const int u = half * (D / 16) + e;
+                        return v + (u >> 3) * C::kHalfBytes +
+                               (((u & 7) ^ (at & (D == 128 ? 7 : 3))) << 4);
+                    };
                     if (key >= cur.keys) {
 #pragma unroll
-                        for (int u = 0; u < D / 8; ++u)
-                            sts128(v + (u >> 3) * C::kHalfBytes + (((u ^ tid) & 7) << 4), 0, 0, 0, 0);
+                        for (int e = 0; e < D / 16; ++e) sts128(chunk(e), 0, 0, 0, 0);
                     } else if (from > 0) {
                         bool odd = false;
 #pragma unroll
-                        for (int u = 0; u < D / 8; ++u) {
-                            const uint32_t at =
-                                v + (u >> 3) * C::kHalfBytes + (((u ^ tid) & 7) << 4);
+                        for (int e = 0; e < D / 16; ++e) {
                             uint32_t x0, x1, x2, x3;
-                            lds128(at, x0, x1, x2, x3);
+                            lds128(chunk(e), x0, x1, x2, x3);
                             if (not_finite(x0) || not_finite(x1) || not_finite(x2) ||
                                 not_finite(x3)) {
                                 odd = true;
-                                sts128(at, finite_or_zero(x0), finite_or_zero(x1),
+                                sts128(chunk(e), finite_or_zero(x0), finite_or_zero(x1),
                                        finite_or_zero(x2), finite_or_zero(x3));
                             }
                         }
                         if (odd) *reinterpret_cast<volatile int *>(&ctl.odd[seg & 1]) = 1;
                     }
                 }
+                // the P buffer is free: with two of them its last product came before this S
+                // in the tensor core's order
                 const uint32_t pb = i % C::kPBufs;
-                await(p_free + 8 * pb, ((i / C::kPBufs) & 1u) ^ 1u);
+                if (C::kPBufs == 1) await(p_free, (i & 1u) ^ 1u);
                 __syncwarp();
-                const uint32_t prow = s0 + C::kP + pb * C::kPBytes + tid * 128;
+                const uint32_t prow = s0 + C::kP + pb * C::kPBytes + at * 128;
                 // weights to shared memory; the largest log2 of one
                 auto weights = [&]() {
                     float top = -INFINITY;
-                    for (int c0 = 0; c0 < n; c0 += 16) {
-                        uint32_t r[16];
-                        float t[16];
-                        tmem_ld_32x32b_x16(col + c0, r);
-                        const float4 *m4 = reinterpret_cast<const float4 *>(m_row + c0);
-                        float4 m[4];
+                    auto eight = [&](const uint32_t (&r)[8], int c) {
+                        const float4 ma = *reinterpret_cast<const float4 *>(m_row + c);
+                        const float4 mb = *reinterpret_cast<const float4 *>(m_row + c + 4);
+                        const float m[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+                        float t[8];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) m[q] = m4[q];
-                        tmem_wait_ld16(r);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            t[4 * q] = fmaf(__uint_as_float(r[4 * q]), sl, -m[q].x);
-                            t[4 * q + 1] = fmaf(__uint_as_float(r[4 * q + 1]), sl, -m[q].y);
-                            t[4 * q + 2] = fmaf(__uint_as_float(r[4 * q + 2]), sl, -m[q].z);
-                            t[4 * q + 3] = fmaf(__uint_as_float(r[4 * q + 3]), sl, -m[q].w);
+                        for (int j = 0; j < 8; ++j) {
+                            t[j] = fmaf(__uint_as_float(r[j]), sl, -m[j]);
+                            if (c + j < from) t[j] = -INFINITY;
                         }
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (c0 + j < from) t[j] = -INFINITY;
+                        for (int j = 0; j < 8; j += 2) top = max3(top, t[j], t[j + 1]);
+                        uint32_t word[4];
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2) top = max3(top, t[j], t[j + 1]);
-                        uint32_t word[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
+                        for (int j = 0; j < 4; ++j)
                             word[j] = pack2_bf16(exp2_approx(t[2 * j]), exp2_approx(t[2 * j + 1]));
-                        const uint32_t to = prow + (c0 >> 6) * (kTileKeys * 128);
-                        const int u = (c0 >> 3) & 7;
-                        sts128(to + ((u ^ (tid & 7)) << 4), word[0], word[1], word[2], word[3]);
-                        sts128(to + (((u + 1) ^ (tid & 7)) << 4), word[4], word[5], word[6], word[7]);
+                        sts128(prow + (c >> 6) * (kTileKeys * 128) +
+                                   ((((c >> 3) & 7) ^ (at & 7)) << 4),
+                               word[0], word[1], word[2], word[3]);
+                    };
+                    for (int c = 8 * half; c < n; c += 32) {
+                        uint32_t ra[8], rb[8];
+                        const bool two = c + 16 < n;
+                        tmem_ld_32x32b_x8(col + c, ra);
+                        if (two) tmem_ld_32x32b_x8(col + c + 16, rb);
+                        tmem_wait_ld8(ra);
+                        eight(ra, c);
+                        if (two) {
+                            tmem_wait_ld8(rb);
+                            eight(rb, c + 16);
+                        }
                     }
                     return top;
                 };
@@ -879,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         await(p_free + 8 * ((i - 1) % C::kPBufs), ((i - 1) / C::kPBufs) & 1u);
                     __syncwarp();
                     tc_fence_after();
-                    for (int c0 = 0; kt > cur.kt && c0 < n; c0 += 16) {
+                    for (int c0 = 16 * half; kt > cur.kt && c0 < n; c0 += 32) {
                         for (uint32_t base : {C::kColO, C::kColL}) {
                             uint32_t r[16];
                             tmem_ld_32x32b_x16(lane_base + base + ob * kN + c0, r);
@@ -915,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Adds up the parts of the unit that starts in CTA blockIdx.x and ends in a later one: with
 // M = max m,  out = sum 2^(m - M) O / sum 2^(m - M) l.  A warp takes a row at a time.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) verify_join_kernel(const Params p)
+__global__ void __launch_bounds__(kJoinThreads, 1) verify_join_kernel(const Params p)
 {
     constexpr int kPer = D / 32;
     wait_for_prior_kernels();
@@ -923,8 +944,7 @@ __global__ void __launch_bounds__(kJoinThreads) verify_join_kernel(const Params 
     const int row0 = unit.x, h = unit.y, rows = unit.z, parts = unit.w;
     if (parts < 2) return;
     const int lane = threadIdx.x & 31;
-    for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
-         r += kJoinSplit * (kJoinThreads / 32)) {
+    for (int r = threadIdx.x >> 5; r < rows; r += kJoinThreads / 32) {
         // part 0 is its CTA's last, the others their CTAs' first
         auto part = [&](int i) {
             return static_cast<size_t>(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kMaxRows + r;
