@@ -98,11 +98,12 @@ struct Cfg {
     static constexpr int kPBufs = kN == 64 ? 2 : 1;
     static constexpr int kTileBytes = kTileKeys * D * 2;
     static constexpr int kHalfBytes = kTileKeys * 128;       // 64 channels of a tile
-    static constexpr int kStages = 4 * (128 / D);
+    static constexpr int kSlots = 2 * (128 / D);             // K tiles, and V tiles, in the ring
     static constexpr int kQBytes = kN * D * 2;
     static constexpr int kPBytes = (kN + 63) / 64 * kTileKeys * 128;
     static constexpr int kRing = 0;
-    static constexpr int kQ = kRing + kStages * kTileBytes;
+    static constexpr int kRingV = kRing + kSlots * kTileBytes;
+    static constexpr int kQ = kRingV + kSlots * kTileBytes;
     static constexpr int kP = kQ + kQBufs * kQBytes;
     static constexpr int kOnes = kP + kPBufs * kPBytes;
     static constexpr int kM = kOnes + kOnesBytes;            // float [2][kN]
@@ -112,12 +113,13 @@ struct Cfg {
     static_assert(kColL + kOBufs * kN <= kTmemCols, "tensor memory");
 };
 
-constexpr int kMaxStages = 8;
+constexpr int kMaxSlots = 4;
 constexpr int kMaxBoxes = kTileKeys / 16;         // pages of a tile at most
 
 struct Ctl {
-    unsigned long long kv_full[kMaxStages], kv_empty[kMaxStages];
-    unsigned long long s_full[2], p_full[2], p_free[2];
+    // by ring slot: K copied, V copied, S made (and K's slot free), O added to (and V's slot free)
+    unsigned long long k_full[kMaxSlots], v_full[kMaxSlots], s_full[kMaxSlots], o_done[kMaxSlots];
+    unsigned long long p_full[2];
     unsigned long long q_full[2], q_empty[2], o_full[2], o_empty[2], drain;
     long long start_off;                          // first place in its request
     unsigned long long sums[kThreads / 32];
@@ -125,6 +127,7 @@ struct Ctl {
     uint32_t tmem;
     int abort;
     int odd[2];                                   // a cleared value, by parity of the segment
+    int seg_n[2], seg_tiles[2];                   // the segment of a Q buffer; no tiles: the end
 };
 
 template <int D, int kN>
@@ -379,20 +382,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 31) ctl.sums[warp] = sum;
     for (int i = tid; i < kOnesBytes / 4; i += kThreads)
         reinterpret_cast<uint32_t *>(smem + C::kOnes)[i] = 0x3F803F80u;
-    const uint32_t kv_full = smem_u32(ctl.kv_full), kv_empty = smem_u32(ctl.kv_empty);
-    const uint32_t s_full = smem_u32(ctl.s_full), p_full = smem_u32(ctl.p_full);
-    const uint32_t p_free = smem_u32(ctl.p_free), q_full = smem_u32(ctl.q_full);
+    const uint32_t k_full = smem_u32(ctl.k_full), v_full = smem_u32(ctl.v_full);
+    const uint32_t s_full = smem_u32(ctl.s_full), o_done = smem_u32(ctl.o_done);
+    const uint32_t p_full = smem_u32(ctl.p_full), q_full = smem_u32(ctl.q_full);
     const uint32_t q_empty = smem_u32(ctl.q_empty), o_full = smem_u32(ctl.o_full);
     const uint32_t o_empty = smem_u32(ctl.o_empty), drain = smem_u32(&ctl.drain);
     if (tid == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(kv_full + 8 * i, 1);
-            mbar_init(kv_empty + 8 * i, 1);
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(k_full + 8 * i, 1);
+            mbar_init(v_full + 8 * i, 1);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(o_done + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(s_full + 8 * i, 1);
             mbar_init(p_full + 8 * i, kSoftThreads);
-            mbar_init(p_free + 8 * i, 1);
             mbar_init(q_full + 8 * i, kQThreads);
             mbar_init(q_empty + 8 * i, 1);
             mbar_init(o_full + 8 * i, 1);
@@ -440,15 +443,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
-    Walk w;
+    Walk w = {};
     bool more = w.begin(p, t1 > t0 ? ctl.start_b : 0, t1 > t0 ? ctl.start_off : 0, t1 - t0);
 
     if (warp == kWarpK || warp == kWarpV) {
         // ---------------------------------------------------- K or V pages into the ring
         const int boxes = kTileKeys / p.ps;       // pages of a tile
-        const void *map = warp == kWarpK ? &tm_k : &tm_v;
-        const uint32_t first = warp == kWarpK ? 0 : 1;
-        uint32_t i = 0;                           // K of tile i is the ring's copy 2 i, V 2 i + 1
+        const bool is_k = warp == kWarpK;
+        const void *map = is_k ? &tm_k : &tm_v;
+        const uint32_t full = is_k ? k_full : v_full, empty = is_k ? s_full : o_done;
+        const uint32_t ring = s0 + (is_k ? C::kRing : C::kRingV);
+        uint32_t i = 0;
         bool ok = true;
         // A segment, and page ids 32 at a time, those after them and the next segment's first
         // on their way meanwhile: a table's line comes from HBM, which is most of a tile's time.
@@ -493,13 +498,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int row[kMaxBoxes];
 #pragma unroll
                 for (int j = 0; j < kMaxBoxes; ++j) row[j] = __shfl_sync(0xFFFFFFFFu, id, j);
-                const uint32_t slot = (2 * i + first) % C::kStages;
-                ok = warp_wait(kv_empty + 8 * slot, (((2 * i + first) / C::kStages) & 1u) ^ 1u, ctl,
-                               p);
+                const uint32_t slot = i % C::kSlots;
+                ok = warp_wait(empty + 8 * slot, ((i / C::kSlots) & 1u) ^ 1u, ctl, p);
                 if (!ok) break;
                 if (elect_one()) {
-                    const uint32_t bar = kv_full + 8 * slot;
-                    uint32_t dst = s0 + C::kRing + slot * C::kTileBytes;
+                    const uint32_t bar = full + 8 * slot;
+                    uint32_t dst = ring + slot * C::kTileBytes;
                     mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n) * p.ps * D * 2);
 #pragma unroll
                     for (int j = 0; j < kMaxBoxes; ++j)
@@ -514,101 +518,87 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++i;
             }
         }
-        // copies land before the CTA ends: this warp's among the ring's last
-        for (uint32_t t = i; t-- > 0;) {
-            const uint32_t c = 2 * t + first;
-            if (c + C::kStages <= 2 * i - 1) break;
-            wait_drain(kv_full + 8 * (c % C::kStages), (c / C::kStages) & 1u, p);
-        }
+        // copies land before the CTA ends
+        for (uint32_t back = 1; back <= C::kSlots && back <= i; ++back)
+            wait_drain(full + 8 * ((i - back) % C::kSlots), ((i - back) / C::kSlots) & 1u, p);
     } else if (warp == kWarpMma) {
         // ---------------------------------------------------- S^T = K Q^T, O^T += V^T P
-        const uint64_t ones = smem_desc(s0 + C::kOnes, 128, 128, kSwizzleNone);
-        struct Tile {
-            uint32_t n;                           // columns
-            uint32_t seg;
-            bool first, last;
-        } prev = {0, 0, false, false};
-        uint32_t i = 0, seg = 0;
-        bool ok = true, any = false;
-        auto values = [&](const Tile &t, uint32_t j) {
-            const uint32_t slot = (2 * j + 1) % C::kStages;
-            const uint32_t pb = j % C::kPBufs, ob = t.seg % C::kOBufs;
-            if (!warp_wait(kv_full + 8 * slot, ((2 * j + 1) / C::kStages) & 1u, ctl, p))
-                return false;
-            if (t.first && !warp_wait(o_empty + 8 * ob,
-                                 ((t.seg / C::kOBufs) & 1u) ^ 1u, ctl, p))
-                return false;
-            if (!warp_wait(p_full + 8 * (j & 1), (j >> 1) & 1u, ctl, p))
-                return false;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t a = smem_desc(s0 + C::kRing + slot * C::kTileBytes, C::kHalfBytes,
-                                             1024, kSwizzle128B);
-                const uint64_t b = smem_desc(s0 + C::kP + pb * C::kPBytes, kTileKeys * 128, 1024,
-                                             kSwizzle128B);
-                const uint32_t id_o = idesc_bf16_f32(D, t.n, 1, 1);
-                const uint32_t id_l = idesc_bf16_f32(64, t.n, 0, 1);
+        // One thread, from start to end: votes and walks of a whole warp took longer than the
+        // MMAs themselves (800 of 1900 cycles a tile with D = 64).
+        if (elect_one()) {
+            const uint64_t ones = smem_desc(s0 + C::kOnes, 128, 128, kSwizzleNone);
+            const uint64_t dk = smem_desc(s0 + C::kRing, 16, 1024, kSwizzle128B);
+            const uint64_t dv = smem_desc(s0 + C::kRingV, C::kHalfBytes, 1024, kSwizzle128B);
+            const uint64_t dq = smem_desc(s0 + C::kQ, 16, 1024, kSwizzle128B);
+            const uint64_t dp = smem_desc(s0 + C::kP, kTileKeys * 128, 1024, kSwizzle128B);
+            uint32_t i = 0, seg = 0;
+            // the tile whose values are to be added: its columns, its segment, first or last of it
+            uint32_t pn = 0, pseg = 0;
+            bool pfirst = false, plast = false, ok = true;
+            auto values = [&]() {
+                const uint32_t j = i - 1, slot = j % C::kSlots, ob = pseg % C::kOBufs;
+                ok = wait(v_full + 8 * slot, (j / C::kSlots) & 1u, ctl, p) &&
+                     (!pfirst ||
+                      wait(o_empty + 8 * ob, ((pseg / C::kOBufs) & 1u) ^ 1u, ctl, p)) &&
+                     wait(p_full + 8 * (j & 1), (j >> 1) & 1u, ctl, p);
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t a = dv + slot * (C::kTileBytes >> 4);
+                const uint64_t b = dp + (j % C::kPBufs) * (C::kPBytes >> 4);
+                const uint32_t to = tmem + C::kColO + ob * kN, tl = tmem + C::kColL + ob * kN;
+                const uint32_t id_o = idesc_bf16_f32(D, pn, 1, 1);
+                const uint32_t id_l = idesc_bf16_f32(64, pn, 0, 1);
 #pragma unroll
                 for (int k = 0; k < kTileKeys / 16; ++k) {
-                    const uint32_t acc = !t.first || k > 0;
-                    umma_bf16(tmem + C::kColO + ob * kN, a + k * 128, b + k * 128, id_o, acc);
-                    umma_bf16(tmem + C::kColL + ob * kN, ones, b + k * 128, id_l, acc);
+                    const uint32_t acc = !pfirst || k > 0;
+                    umma_bf16(to, a + k * 128, b + k * 128, id_o, acc);
+                    umma_bf16(tl, ones, b + k * 128, id_l, acc);
                 }
-                umma_commit(kv_empty + 8 * slot);
-                umma_commit(p_free + 8 * pb);
-                if (t.last) umma_commit(o_full + 8 * ob);
-            }
-            __syncwarp();
-            return true;
-        };
-        while (more && ok) {
-            const uint32_t n = (w.unit_rows(p) + 15) & ~15;
-            for (int kt = w.kt; kt < w.kt_end && ok; ++kt) {
-                const bool first = kt == w.kt, last = kt + 1 == w.kt_end;
-                const uint32_t slot = (2 * i) % C::kStages, qb = seg % C::kQBufs;
-                ok = (!first || warp_wait(q_full + 8 * qb, (seg / C::kQBufs) & 1u,
-                                     ctl, p)) &&
-                     warp_wait(kv_full + 8 * slot, ((2 * i) / C::kStages) & 1u, ctl,
-                          p);
+                umma_commit(o_done + 8 * slot);
+                if (plast) umma_commit(o_full + 8 * ob);
+            };
+            for (; ok; ++seg) {
+                const uint32_t qb = seg % C::kQBufs;
+                if (!wait(q_full + 8 * qb, (seg / C::kQBufs) & 1u, ctl, p)) ok = false;
                 if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t a = smem_desc(s0 + C::kRing + slot * C::kTileBytes, 16, 1024,
-                                                 kSwizzle128B);
-                    const uint64_t b = smem_desc(s0 + C::kQ + qb * C::kQBytes, 16, 1024,
-                                                 kSwizzle128B);
-                    const uint32_t id = idesc_bf16_f32(kTileKeys, n, 0, 0);
+                const uint32_t n = ctl.seg_n[qb];
+                const int tiles = ctl.seg_tiles[qb];
+                if (tiles == 0) break;
+                const uint32_t id = idesc_bf16_f32(kTileKeys, n, 0, 0);
+                const uint64_t b = dq + qb * (C::kQBytes >> 4);
+                for (int t = 0; t < tiles; ++t) {
+                    const uint32_t slot = i % C::kSlots;
+                    if (!wait(k_full + 8 * slot, (i / C::kSlots) & 1u, ctl, p)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t a = dk + slot * (C::kTileBytes >> 4);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         umma_bf16(tmem + C::kColS + (i & 1) * kN,
                                   a + (k >> 2) * (C::kHalfBytes >> 4) + (k & 3) * 2,
                                   b + (k >> 2) * (kN * 128 >> 4) + (k & 3) * 2, id, k > 0);
-                    umma_commit(kv_empty + 8 * slot);
-                    umma_commit(s_full + 8 * (i & 1));
-                    if (last) umma_commit(q_empty + 8 * qb);
+                    umma_commit(s_full + 8 * slot);
+                    if (t + 1 == tiles) umma_commit(q_empty + 8 * qb);
+                    if (i > 0) values();
+                    if (!ok) break;
+                    pn = n, pseg = seg, pfirst = t == 0, plast = t + 1 == tiles;
+                    ++i;
                 }
-                __syncwarp();
-                any = true;
-                if (i > 0) ok = values(prev, i - 1);
-                prev = Tile{n, seg, first, last};
-                ++i;
             }
-            ++seg;
-            more = w.next(p);
-        }
-        if (ok && i > 0) values(prev, i - 1);
-        if (any) {                                // MMAs finish before the CTA ends
-            if (elect_one()) umma_commit(drain);
-            __syncwarp();
+            if (ok && i > 0) values();
+            umma_commit(drain);                   // MMAs finish before the CTA ends
             wait_drain(drain, 0, p);
         }
+        __syncwarp();
     } else if (warp >= kWarpQ) {
         // ---------------------------------------------------- Q rows of each segment
         const int t = tid - kWarpQ * 32;
         uint32_t seg = 0;
-        while (more) {
+        for (;;) {
             const uint32_t qb = seg % C::kQBufs;
-            const int rows = w.unit_rows(p), n = (rows + 15) & ~15;
+            const int rows = more ? w.unit_rows(p) : 0, n = (rows + 15) & ~15;
             if (!warp_wait(q_empty + 8 * qb, ((seg / C::kQBufs) & 1u) ^ 1u, ctl, p))
                 break;
             const uint32_t dst = s0 + C::kQ + qb * C::kQBytes;
@@ -628,7 +618,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             cp_async_wait_all();
             fence_proxy_async_smem();
+            if (lane == 0) {
+                ctl.seg_n[qb] = n;
+                ctl.seg_tiles[qb] = more ? w.kt_end - w.kt : 0;
+            }
             mbar_arrive(q_full + 8 * qb);
+            if (!more) break;
             ++seg;
             more = w.next(p);
         }
@@ -795,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int from = 0;
                 if (key >= cur.keys) from = kMaxRows;
                 else if (key >= cur.hidden) from = (key - cur.hidden + 1) * p.group;
-                await(s_full + 8 * (i & 1), (i >> 1) & 1u);
+                await(s_full + 8 * (i % C::kSlots), (i / C::kSlots) & 1u);
                 __syncwarp();
                 tc_fence_after();
                 const bool masked = (kt + 1) * kTileKeys > cur.hidden;
@@ -813,11 +808,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (masked) {
                     // values behind the last key, and those that are not finite
-                    const uint32_t slot = (2 * i + 1) % C::kStages;
-                    await(kv_full + 8 * slot, ((2 * i + 1) / C::kStages) & 1u);
+                    const uint32_t slot = i % C::kSlots;
+                    await(v_full + 8 * slot, (i / C::kSlots) & 1u);
                     // 16-byte chunks, a half of the row each, in an order of the lane's own, so
                     // that neighbouring rows, 128 bytes apart, meet different banks
-                    const uint32_t v = s0 + C::kRing + slot * C::kTileBytes + at * 128;
+                    const uint32_t v = s0 + C::kRingV + slot * C::kTileBytes + at * 128;
                     auto chunk = [&](int e) {
                         const int u = half * (D / 16) + e;
                         return v + (u >> 3) * C::kHalfBytes +
@@ -845,7 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the P buffer is free: with two of them its last product came before this S
                 // in the tensor core's order
                 const uint32_t pb = i % C::kPBufs;
-                if (C::kPBufs == 1) await(p_free, (i & 1u) ^ 1u);
+                if (C::kPBufs == 1 && i > 0)
+                    await(o_done + 8 * ((i - 1) % C::kSlots), ((i - 1) / C::kSlots) & 1u);
                 __syncwarp();
                 const uint32_t prow = s0 + C::kP + pb * C::kPBytes + at * 128;
                 // weights to shared memory; the largest log2 of one
@@ -897,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     soft_sync();
                     const uint32_t ob = seg % C::kOBufs;
                     if (kt > cur.kt)
-                        await(p_free + 8 * ((i - 1) % C::kPBufs), ((i - 1) / C::kPBufs) & 1u);
+                        await(o_done + 8 * ((i - 1) % C::kSlots), ((i - 1) / C::kSlots) & 1u);
                     __syncwarp();
                     tc_fence_after();
                     for (int c0 = 16 * half; kt > cur.kt && c0 < n; c0 += 32) {
