@@ -32,11 +32,11 @@
 // border leave (m, l, O) in the workspace, and verify_join_kernel adds the parts up, in
 // order, so results do not depend on timing.  It is launched to overlap with this kernel's end.
 //
-// Warps: 0-7 softmax and output (two threads to a key of the tile, later to a channel of the
-// output, each with half of the rows), 8 and 9 copy K and V pages into a ring of 32 KB tiles by
-// TMA (one box a page and 64 channels; one warp for both took 90 cycles a box, 3000 of a
-// tile's 2800 with pages of 16), 10 issues the MMAs, 11 copies Q.  S and P are double-buffered, so S of the next tile and O of the last run
-// beside the softmax; a unit's output is written after the next unit's first softmax.
+// Warps: 0-3 and 4-7 softmax and output (thread = key of the tile, then channel of the output),
+// the groups taking tiles in turn, 8 and 9 copy K and V pages into rings of 32 KB tiles by TMA
+// (one box a page and 64 channels; one warp for both took 90 cycles a box, 3000 of a tile's
+// 2800 with pages of 16), 10 issues the MMAs, 11 copies Q.  S and P are double-buffered, so S of
+// the next tile and O of the last run beside the softmax.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -54,7 +54,7 @@ constexpr int kMaxB = 4096;
 constexpr int kMaxCtas = 160;                     // grid: one CTA per SM, at most this many
 constexpr int kMaxRows = 112;                     // rows of a query tile
 constexpr int kThreads = 384;
-constexpr int kSoftThreads = 256;
+constexpr int kSoftThreads = 128;               // of each of the two softmax groups
 constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpQ = 11;
 constexpr int kQThreads = 32;
 constexpr uint32_t kTmemCols = 512;
@@ -88,14 +88,12 @@ __host__ __device__ inline Layout workspace_layout(int D)
     return w;
 }
 
-// kN: rows of a query tile at most.  Beside 64 rows fit four ring tiles of 32 KB and two
-// buffers of everything; beside 112, four tiles and one buffer of P and of O (a fifth tile
-// gains nothing).
+// kN: rows of a query tile at most.  Beside 64 rows fit two buffers of Q and of O; beside 112,
+// one of each.
 template <int D, int kN>
 struct Cfg {
-    static constexpr int kQBufs = 2;
+    static constexpr int kQBufs = kN == 64 ? 2 : 1;
     static constexpr int kOBufs = kN == 64 ? 2 : 1;
-    static constexpr int kPBufs = kN == 64 ? 2 : 1;
     static constexpr int kTileBytes = kTileKeys * D * 2;
     static constexpr int kHalfBytes = kTileKeys * 128;       // 64 channels of a tile
     static constexpr int kSlots = 2 * (128 / D);             // K tiles, and V tiles, in the ring
@@ -105,10 +103,10 @@ struct Cfg {
     static constexpr int kRingV = kRing + kSlots * kTileBytes;
     static constexpr int kQ = kRingV + kSlots * kTileBytes;
     static constexpr int kP = kQ + kQBufs * kQBytes;
-    static constexpr int kOnes = kP + kPBufs * kPBytes;
+    static constexpr int kOnes = kP + 2 * kPBytes;
     static constexpr int kM = kOnes + kOnesBytes;            // float [2][kN]
-    static constexpr int kRed = kM + 2 * kN * 4;             // float [4][kN]
-    static constexpr int kCtl = kRed + 4 * kN * 4;
+    static constexpr int kRed = kM + 2 * kN * 4;             // float [2 groups][4][kN]
+    static constexpr int kCtl = kRed + 2 * 4 * kN * 4;
     static constexpr uint32_t kColS = 0, kColO = 2 * kN, kColL = kColO + kOBufs * kN;
     static_assert(kColL + kOBufs * kN <= kTmemCols, "tensor memory");
 };
@@ -119,13 +117,14 @@ constexpr int kMaxBoxes = kTileKeys / 16;         // pages of a tile at most
 struct Ctl {
     // by ring slot: K copied, V copied, S made (and K's slot free), O added to (and V's slot free)
     unsigned long long k_full[kMaxSlots], v_full[kMaxSlots], s_full[kMaxSlots], o_done[kMaxSlots];
-    unsigned long long p_full[2];
+    unsigned long long p_full[2], m_full[2];
     unsigned long long q_full[2], q_empty[2], o_full[2], o_empty[2], drain;
     long long start_off;                          // first place in its request
     unsigned long long sums[kThreads / 32];
     int start_b;
     uint32_t tmem;
     int abort;
+    int epoch;                                    // times that a reference m rose
     int odd[2];                                   // a cleared value, by parity of the segment
     int seg_n[2], seg_tiles[2];                   // the segment of a Q buffer; no tiles: the end
 };
@@ -265,18 +264,22 @@ struct Walk {
     __device__ __forceinline__ int keys(const Params &p) const { return request(p).keys(qt); }
 };
 
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 2, 256;" ::: "memory"); }
+// Barrier of a softmax group's 128 threads (named barriers 2 and 3).
+__device__ __forceinline__ void group_sync(int group)
+{
+    asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
+}
 
-__device__ __forceinline__ bool soft_any(bool v)
+__device__ __forceinline__ bool group_any(int group, bool v)
 {
     uint32_t any;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 2, 256, p;\n\t"
+        "bar.red.or.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(any)
-        : "r"(static_cast<uint32_t>(v))
+        : "r"(static_cast<uint32_t>(v)), "r"(2 + group)
         : "memory");
     return any != 0;
 }
@@ -293,6 +296,20 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+// t = s scale - m for two rows (fma.rn.f32x2)
+__device__ __forceinline__ void scaled2(float &t0, float &t1, uint32_t s0, uint32_t s1, float scale,
+                                        float m0, float m1)
+{
+    asm("{\n\t.reg .b64 rs, rc, rm, rt;\n\t"
+        "mov.b64 rs, {%2, %3};\n\t"
+        "mov.b64 rc, {%4, %4};\n\t"
+        "mov.b64 rm, {%5, %6};\n\t"
+        "fma.rn.f32x2 rt, rs, rc, rm;\n\t"
+        "mov.b64 {%0, %1}, rt;\n\t}"
+        : "=f"(t0), "=f"(t1)
+        : "f"(__uint_as_float(s0)), "f"(__uint_as_float(s1)), "f"(scale), "f"(-m0), "f"(-m1));
 }
 
 __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi)
@@ -384,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         reinterpret_cast<uint32_t *>(smem + C::kOnes)[i] = 0x3F803F80u;
     const uint32_t k_full = smem_u32(ctl.k_full), v_full = smem_u32(ctl.v_full);
     const uint32_t s_full = smem_u32(ctl.s_full), o_done = smem_u32(ctl.o_done);
-    const uint32_t p_full = smem_u32(ctl.p_full), q_full = smem_u32(ctl.q_full);
+    const uint32_t p_full = smem_u32(ctl.p_full), m_full = smem_u32(ctl.m_full);
+    const uint32_t q_full = smem_u32(ctl.q_full);
     const uint32_t q_empty = smem_u32(ctl.q_empty), o_full = smem_u32(ctl.o_full);
     const uint32_t o_empty = smem_u32(ctl.o_empty), drain = smem_u32(&ctl.drain);
     if (tid == 0) {
@@ -396,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(p_full + 8 * i, kSoftThreads);
+            mbar_init(m_full + 8 * i, kSoftThreads);
             mbar_init(q_full + 8 * i, kQThreads);
             mbar_init(q_empty + 8 * i, 1);
             mbar_init(o_full + 8 * i, 1);
@@ -404,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(drain, 1);
         mbar_fence_init();
         ctl.abort = 0;
+        ctl.epoch = 0;
         ctl.odd[0] = ctl.odd[1] = 0;
     }
     if (warp == kWarpMma) {
@@ -544,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t a = dv + slot * (C::kTileBytes >> 4);
-                const uint64_t b = dp + (j % C::kPBufs) * (C::kPBytes >> 4);
+                const uint64_t b = dp + (j & 1) * (C::kPBytes >> 4);
                 const uint32_t to = tmem + C::kColO + ob * kN, tl = tmem + C::kColL + ob * kN;
                 const uint32_t id_o = idesc_bf16_f32(D, pn, 1, 1);
                 const uint32_t id_l = idesc_bf16_f32(64, pn, 0, 1);
@@ -629,10 +649,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------------------------------------------- softmax and output
+        // Group 0 takes the CTA's even tiles, group 1 the odd ones, so that one's exponentials
+        // run beside the other's waits and barriers (both on one tile, half of the rows each,
+        // took as long as one alone).  They share m and O, so tiles are handed to the MMA in
+        // their order: a group waits for the one before its own, and makes its weights anew
+        // if m rose meanwhile.
+        const int wg = warp >> 2, quad = warp & 3, at = tid & 127;
         float *m_s = reinterpret_cast<float *>(smem + C::kM);
-        float *red = reinterpret_cast<float *>(smem + C::kRed);
-        // warps w and w + 4 read the same 32 lanes, keys or channels, and take 8 or 16 rows in turn
-        const int quad = warp & 3, half = warp >> 2, at = tid & 127;
+        float *red = reinterpret_cast<float *>(smem + C::kRed) + wg * 4 * kN;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         // the output's channel of this thread (M = 64 puts 16 rows in each warp's lanes)
         const int d = D == 128 ? at : quad * 16 + (lane & 15);
@@ -641,8 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         struct Seg {
             int row0, rows, h, kt, kt_end, keys, hidden, b;   // hidden: keys that row 0 sees
             bool starts, ends;
-            int parts;
-        } cur = {}, done = {};
+        } cur = {};
         int4 desc = make_int4(0, 0, 0, 0);
 
         // after a wait that ran out the warps go on without waiting, so that they meet at the
@@ -662,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int part = 2 * blockIdx.x + (s.starts ? 1 : 0);
             const bool odd = *reinterpret_cast<volatile int *>(&ctl.odd[seg & 1]);
             // a thread per row: 1 / l and the row's place in the output, or (m, l)
-            for (int c0 = 16 * warp; c0 < s.rows; c0 += 128) {
+            for (int c0 = 16 * quad; c0 < s.rows; c0 += 64) {
                 uint32_t l[16];
                 tmem_ld_32x32b_x16(lane_base + C::kColL + ob * kN + c0, l);
                 tmem_wait_ld16(l);
@@ -670,21 +693,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) red[c0 + j] = __uint_as_float(l[j]);
             }
-            soft_sync();
-            if (tid < s.rows) {
-                const float l = red[tid];
+            group_sync(wg);
+            if (at < s.rows) {
+                const float l = red[at];
                 if (direct) {
-                    const int i = tid / p.group;
-                    red[kN + tid] = __int_as_float(i * p.Hq + tid - i * p.group);
-                    red[tid] = 1.0f / l;
+                    const int i = at / p.group;
+                    red[kN + at] = __int_as_float(i * p.Hq + at - i * p.group);
+                    red[at] = 1.0f / l;
                 } else {
-                    p.part_ml[static_cast<size_t>(part) * kMaxRows + tid] =
-                        make_float2(m_s[(seg & 1) * kN + tid], l);
+                    p.part_ml[static_cast<size_t>(part) * kMaxRows + at] =
+                        make_float2(m_s[(seg & 1) * kN + at], l);
                 }
             }
-            soft_sync();
+            group_sync(wg);
             const size_t row0 = static_cast<size_t>(s.row0) * p.Hq + static_cast<size_t>(s.h) * p.group;
-            for (int c0 = 16 * half; c0 < s.rows; c0 += 32) {
+            for (int c0 = 0; c0 < s.rows; c0 += 16) {
                 uint32_t o[16];
                 float v[16];
                 tmem_ld_32x32b_x16(lane_base + C::kColO + ob * kN + c0, o);
@@ -735,7 +758,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (c0 + j < s.rows) to[j * D] = v[j];
                 }
             }
-            soft_sync();                          // red is free again
+            group_sync(wg);                       // red is free again
+            if (at == 0) ctl.odd[seg & 1] = 0;
             tc_fence_before();
             mbar_arrive(o_empty + 8 * ob);
         };
@@ -748,10 +772,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c0 + j < from) t[j] = -INFINITY;
             }
         };
-        // red[q][row] = the tile's maximum in the keys of lanes 32 q on; `share`: rows 16 w on in
-        // warp w's keys alone
+        // red[q][row] = the tile's maximum in the keys of warp q; `share`: in that of one warp
         auto reduce = [&](uint32_t col, int n, int from, bool share) {
-            for (int c0 = 16 * (share ? warp : half); c0 < n; c0 += share ? 128 : 32) {
+            for (int c0 = share ? 16 * quad : 0; c0 < n; c0 += share ? 64 : 16) {
                 uint32_t r[16];
                 float t[16];
                 tmem_ld_32x32b_x16(col + c0, r);
@@ -783,145 +806,156 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  vplan::cta_of(T, t1 - 1 + (w.tiles - w.kt_end), G) - cta + 1);
             const int n = (cur.rows + 15) & ~15;
             float *m_row = m_s + (seg & 1) * kN;
-            for (int kt = cur.kt; kt < cur.kt_end; ++kt) {
-                const uint32_t col = lane_base + C::kColS + (i & 1) * kN;
+            int kt = cur.kt + ((i & 1) == static_cast<uint32_t>(wg) ? 0 : 1);
+            i += kt - cur.kt;
+            for (; kt < cur.kt_end; kt += 2, i += 2) {
+                const uint32_t col = lane_base + C::kColS + wg * kN;
                 const int key = kt * kTileKeys + at;
                 // rows from `from` on see this thread's key
                 int from = 0;
                 if (key >= cur.keys) from = kMaxRows;
                 else if (key >= cur.hidden) from = (key - cur.hidden + 1) * p.group;
+                const bool masked = (kt + 1) * kTileKeys > cur.hidden;
+                const bool first = kt == cur.kt;
+                const uint32_t before = p_full + 8 * (wg ^ 1), before_phase = ((i - 1) >> 1) & 1u;
                 await(s_full + 8 * (i % C::kSlots), (i / C::kSlots) & 1u);
+                // m of this segment: to be set here, once the other group has left the tile
+                // before (and what it still read of older segments), or set by the other
+                if (!first) await(m_full + 8 * (seg & 1), (seg >> 1) & 1u);
+                else if (i > 0) await(before, before_phase);
                 __syncwarp();
                 tc_fence_after();
-                const bool masked = (kt + 1) * kTileKeys > cur.hidden;
-                if (kt == cur.kt) {
-                    // m: the maximum over the first tile, or, where every row sees all of it,
-                    // over one warp's 32 keys, which does as well and is one exchange for a warp
-                    reduce(col, n, from, !masked);
-                    soft_sync();
-                    if (tid < n) {
-                        const float m = masked ? max_of(tid) : red[((tid >> 4) & 3) * kN + tid];
-                        m_row[tid] = m == -INFINITY ? 0.0f : m;
-                    }
-                    if (tid == 0) ctl.odd[seg & 1] = 0;
-                    soft_sync();
-                }
                 if (masked) {
                     // values behind the last key, and those that are not finite
                     const uint32_t slot = i % C::kSlots;
                     await(v_full + 8 * slot, (i / C::kSlots) & 1u);
-                    // 16-byte chunks, a half of the row each, in an order of the lane's own, so
-                    // that neighbouring rows, 128 bytes apart, meet different banks
+                    // 16-byte chunks in an order of the lane's own, so that neighbouring rows,
+                    // 128 bytes apart, meet different banks
                     const uint32_t v = s0 + C::kRingV + slot * C::kTileBytes + at * 128;
-                    auto chunk = [&](int e) {
-                        const int u = half * (D / 16) + e;
-                        return v + (u >> 3) * C::kHalfBytes +
-                               (((u & 7) ^ (at & (D == 128 ? 7 : 3))) << 4);
+                    auto chunk = [&](int u) {
+                        return v + (u >> 3) * C::kHalfBytes + (((u ^ at) & 7) << 4);
                     };
                     if (key >= cur.keys) {
 #pragma unroll
-                        for (int e = 0; e < D / 16; ++e) sts128(chunk(e), 0, 0, 0, 0);
+                        for (int u = 0; u < D / 8; ++u) sts128(chunk(u), 0, 0, 0, 0);
                     } else if (from > 0) {
                         bool odd = false;
-#pragma unroll
-                        for (int e = 0; e < D / 16; ++e) {
+#pragma unroll 4
+                        for (int u = 0; u < D / 8; ++u) {
                             uint32_t x0, x1, x2, x3;
-                            lds128(chunk(e), x0, x1, x2, x3);
+                            lds128(chunk(u), x0, x1, x2, x3);
                             if (not_finite(x0) || not_finite(x1) || not_finite(x2) ||
                                 not_finite(x3)) {
                                 odd = true;
-                                sts128(chunk(e), finite_or_zero(x0), finite_or_zero(x1),
+                                sts128(chunk(u), finite_or_zero(x0), finite_or_zero(x1),
                                        finite_or_zero(x2), finite_or_zero(x3));
                             }
                         }
                         if (odd) *reinterpret_cast<volatile int *>(&ctl.odd[seg & 1]) = 1;
                     }
-                }
-                // the P buffer is free: with two of them its last product came before this S
-                // in the tensor core's order
-                const uint32_t pb = i % C::kPBufs;
-                if (C::kPBufs == 1 && i > 0)
-                    await(o_done + 8 * ((i - 1) % C::kSlots), ((i - 1) / C::kSlots) & 1u);
-                __syncwarp();
-                const uint32_t prow = s0 + C::kP + pb * C::kPBytes + at * 128;
-                // weights to shared memory; the largest log2 of one
-                auto weights = [&]() {
-                    float top = -INFINITY;
-                    auto eight = [&](const uint32_t (&r)[8], int c) {
-                        const float4 ma = *reinterpret_cast<const float4 *>(m_row + c);
-                        const float4 mb = *reinterpret_cast<const float4 *>(m_row + c + 4);
-                        const float m[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
-                        float t[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            t[j] = fmaf(__uint_as_float(r[j]), sl, -m[j]);
-                            if (c + j < from) t[j] = -INFINITY;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 8; j += 2) top = max3(top, t[j], t[j + 1]);
-                        uint32_t word[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            word[j] = pack2_bf16(exp2_approx(t[2 * j]), exp2_approx(t[2 * j + 1]));
-                        sts128(prow + (c >> 6) * (kTileKeys * 128) +
-                                   ((((c >> 3) & 7) ^ (at & 7)) << 4),
-                               word[0], word[1], word[2], word[3]);
-                    };
-                    for (int c = 8 * half; c < n; c += 32) {
-                        uint32_t ra[8], rb[8];
-                        const bool two = c + 16 < n;
-                        tmem_ld_32x32b_x8(col + c, ra);
-                        if (two) tmem_ld_32x32b_x8(col + c + 16, rb);
-                        tmem_wait_ld8(ra);
-                        eight(ra, c);
-                        if (two) {
-                            tmem_wait_ld8(rb);
-                            eight(rb, c + 16);
-                        }
-                    }
-                    return top;
-                };
-                if (soft_any(weights() > kRaise)) {
-                    // m rises: O and l of the tiles before are scaled, the weights made anew
-                    reduce(col, n, from, false);
-                    soft_sync();
-                    if (tid < n) {
-                        const float old = m_row[tid], now = fmaxf(old, max_of(tid));
-                        m_row[tid] = now;
-                        red[tid] = exp2_approx(old - now);
-                    }
-                    soft_sync();
-                    const uint32_t ob = seg % C::kOBufs;
-                    if (kt > cur.kt)
-                        await(o_done + 8 * ((i - 1) % C::kSlots), ((i - 1) / C::kSlots) & 1u);
                     __syncwarp();
-                    tc_fence_after();
-                    for (int c0 = 16 * half; kt > cur.kt && c0 < n; c0 += 32) {
-                        for (uint32_t base : {C::kColO, C::kColL}) {
-                            uint32_t r[16];
-                            tmem_ld_32x32b_x16(lane_base + base + ob * kN + c0, r);
-                            tmem_wait_ld16(r);
+                }
+                // The P buffer is free: its last product, two tiles ago, came before this S in the
+                // tensor core's order.
+                const uint32_t prow = s0 + C::kP + wg * C::kPBytes + at * 128;
+                // 1: m has to be set, 2: to be raised.  m is the maximum over the first tile, or,
+                // where every row sees all of it, over one warp's 32 keys, which does as well and
+                // is one exchange for a warp.
+                int task = first ? 1 : 0;
+                for (int tries = 0; tries < 8; ++tries) {
+                    if (task) {
+                        const bool share = task == 1 && !masked;
+                        reduce(col, n, from, share);
+                        group_sync(wg);
+                        if (at < n) {
+                            const float m = share ? red[((at >> 4) & 3) * kN + at] : max_of(at);
+                            if (task == 1) {
+                                m_row[at] = m == -INFINITY ? 0.0f : m;
+                            } else {
+                                const float old = m_row[at], now = fmaxf(old, m);
+                                m_row[at] = now;
+                                red[at] = exp2_approx(old - now);
+                            }
+                        }
+                        group_sync(wg);
+                        if (task == 1) {
+                            mbar_arrive(m_full + 8 * (seg & 1));
+                        } else {                  // the new m first, then word of it
+                            if (at == 0)
+                                *reinterpret_cast<volatile int *>(&ctl.epoch) = ctl.epoch + 1;
+                            group_sync(wg);
+                        }
+                    }
+                    if (task == 2 && !first) {
+                        // O and l of the tiles before are scaled
+                        const uint32_t ob = seg % C::kOBufs;
+                        await(o_done + 8 * ((i - 1) % C::kSlots), ((i - 1) / C::kSlots) & 1u);
+                        __syncwarp();
+                        tc_fence_after();
+                        for (int c0 = 0; c0 < n; c0 += 16) {
+                            for (uint32_t base : {C::kColO, C::kColL}) {
+                                uint32_t r[16];
+                                tmem_ld_32x32b_x16(lane_base + base + ob * kN + c0, r);
+                                tmem_wait_ld16(r);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    r[j] = __float_as_uint(__uint_as_float(r[j]) * red[c0 + j]);
+                                tmem_st_32x32b_x16(lane_base + base + ob * kN + c0, r);
+                            }
+                        }
+                        tmem_wait_st();
+                    }
+                    // weights to shared memory; the largest log2 of one
+                    const int epoch = *reinterpret_cast<volatile int *>(&ctl.epoch);
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < n; c += 16) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(col + c, r);
+                        float4 m[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            m[q] = *reinterpret_cast<const float4 *>(m_row + c + 4 * q);
+                        tmem_wait_ld16(r);
+                        float t[16];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            scaled2(t[4 * q], t[4 * q + 1], r[4 * q], r[4 * q + 1], sl, m[q].x,
+                                    m[q].y);
+                            scaled2(t[4 * q + 2], t[4 * q + 3], r[4 * q + 2], r[4 * q + 3], sl,
+                                    m[q].z, m[q].w);
+                        }
+                        if (masked) {
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
-                                r[j] = __float_as_uint(__uint_as_float(r[j]) * red[c0 + j]);
-                            tmem_st_32x32b_x16(lane_base + base + ob * kN + c0, r);
+                                if (c + j < from) t[j] = -INFINITY;
                         }
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) top = max3(top, t[j], t[j + 1]);
+                        uint32_t word[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            word[j] = pack2_bf16(exp2_approx(t[2 * j]), exp2_approx(t[2 * j + 1]));
+                        const uint32_t to = prow + (c >> 6) * (kTileKeys * 128);
+                        const int u = (c >> 3) & 7;
+                        sts128(to + ((u ^ (at & 7)) << 4), word[0], word[1], word[2], word[3]);
+                        sts128(to + (((u + 1) ^ (at & 7)) << 4), word[4], word[5], word[6], word[7]);
                     }
-                    tmem_wait_st();
-                    weights();
-                    soft_sync();                  // red is free again
+                    // this tile's turn, and what has become of m
+                    if (!first) await(before, before_phase);
+                    const bool stale = *reinterpret_cast<volatile int *>(&ctl.epoch) != epoch;
+                    if (!group_any(wg, stale || top > kRaise)) break;
+                    task = group_any(wg, stale) ? 0 : 2;
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(p_full + 8 * (i & 1));
-                ++i;
-                if (kt == cur.kt && seg > 0) output(done, seg - 1);
+                mbar_arrive(p_full + 8 * wg);
+                if (kt + 1 == cur.kt_end) output(cur, seg);
             }
-            done = cur;
+            i -= kt - cur.kt_end;                 // the next segment's first tile
             ++seg;
             more = w.next(p);
         }
-        if (seg > 0) output(done, seg - 1);
         if (tid == 0) p.desc[blockIdx.x] = desc;
     }
     tc_fence_before();
