@@ -867,7 +867,7 @@ int dspark_verify_attention(const void *q, const void *k_cache, const void *v_ca
     if (cudaGetLastError() != cudaSuccess) return DSPARK_CUDA_ERROR;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = dim3(grid, A::kJoinSplit);
     cfg.blockDim = dim3(A::kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -61,7 +61,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWaitHintNs = 20000;
 constexpr float kRaise = 24.0f;                   // log2 of the weight at which m rises
 constexpr int kOnesBytes = 1152;                  // 8 x 2 core matrices of 128 B, one apart
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinSplit = 4;                     // CTAs that share a unit's rows
+constexpr int kJoinAhead = 8;                     // parts whose O a row has in flight
 
 struct Params {
     const uint16_t *q, *k_cache, *v_cache;
@@ -964,9 +966,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Adds up the parts of the unit that starts in CTA blockIdx.x and ends in a later one: with
-// M = max m,  out = sum 2^(m - M) O / sum 2^(m - M) l.  A warp takes a row at a time.
+// M = max m over the parts,  out = sum 2^(m - M) O / sum 2^(m - M) l.  What bounds it: latency, of
+// three loads that need one another if nothing is done about it.  So every row has a warp of its
+// own (kJoinSplit CTAs to a unit), lane i holds part i's (m, l), and O is fetched beside them.
+// Added up by one CTA of 16 warps a unit, the parts of the benchmark's long request took
+// 15 us after the attention's last CTA.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads, 1) verify_join_kernel(const Params p)
+__global__ void __launch_bounds__(kJoinThreads) verify_join_kernel(const Params p)
 {
     constexpr int kPer = D / 32;
     wait_for_prior_kernels();
@@ -974,38 +980,56 @@ __global__ void __launch_bounds__(kJoinThreads, 1) verify_join_kernel(const Para
     const int row0 = unit.x, h = unit.y, rows = unit.z, parts = unit.w;
     if (parts < 2) return;
     const int lane = threadIdx.x & 31;
-    for (int r = threadIdx.x >> 5; r < rows; r += kJoinThreads / 32) {
+    for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
+         r += kJoinSplit * (kJoinThreads / 32)) {
         // part 0 is its CTA's last, the others their CTAs' first
         auto part = [&](int i) {
             return static_cast<size_t>(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kMaxRows + r;
         };
-        float m = -INFINITY;
-        for (int i = lane; i < parts; i += 32) {
+        auto fetch = [&](int i, float (&v)[kPer]) {
+            const float *o = p.part_o + part(i) * D + lane * kPer;
+            if constexpr (kPer == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(o);
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(o);
+                v[0] = x.x, v[1] = x.y;
+            }
+        };
+        float v[kJoinAhead][kPer];
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i)
+            if (i < parts) fetch(i, v[i]);
+        // M over all parts; a part without l saw no key
+        float2 ml = make_float2(0.0f, 0.0f);
+        if (lane < parts) ml = p.part_ml[part(lane)];
+        float m = ml.y != 0.0f ? ml.x : -INFINITY;
+        for (int i = 32 + lane; i < parts; i += 32) {
             const float2 x = p.part_ml[part(i)];
-            if (x.y > 0.0f || x.y != x.y) m = fmaxf(m, x.x);
+            if (x.y != 0.0f) m = fmaxf(m, x.x);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         float l = 0.0f, acc[kPer] = {};
-#pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
-            const float2 x = p.part_ml[part(i)];
-            if (x.y == 0.0f) continue;            // no key of this part is seen
-            const float f = exp2_approx(x.x - m);
-            l = fmaf(x.y, f, l);
-            const float *o = p.part_o + part(i) * D + lane * kPer;
-            if (kPer == 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(o);
-                acc[0] = fmaf(v.x, f, acc[0]);
-                acc[1] = fmaf(v.y, f, acc[1]);
-                acc[2 % kPer] = fmaf(v.z, f, acc[2 % kPer]);
-                acc[3 % kPer] = fmaf(v.w, f, acc[3 % kPer]);
-            } else {
-                const float2 v = *reinterpret_cast<const float2 *>(o);
-                acc[0] = fmaf(v.x, f, acc[0]);
-                acc[1] = fmaf(v.y, f, acc[1]);
+        for (int i0 = 0; i0 < parts; i0 += 32) {
+            if (i0 > 0) {
+                ml = make_float2(0.0f, 0.0f);
+                if (i0 + lane < parts) ml = p.part_ml[part(i0 + lane)];
+            }
+            const float f = ml.y != 0.0f ? exp2_approx(ml.x - m) : 0.0f;
+            l += ml.y * f;
+            for (int g = i0; g < min(i0 + 32, parts); g += kJoinAhead) {
+#pragma unroll
+                for (int e = 0; e < kJoinAhead; ++e) {
+                    const float w = __shfl_sync(0xFFFFFFFFu, f, g + e - i0);
+                    if (g + e < parts && w != 0.0f)
+#pragma unroll
+                        for (int j = 0; j < kPer; ++j) acc[j] = fmaf(v[e][j], w, acc[j]);
+                    if (g + e + kJoinAhead < parts) fetch(g + e + kJoinAhead, v[e]);
+                }
             }
         }
+        l = warp_sum(l);
         const float inv = 1.0f / l;
         uint32_t *to = reinterpret_cast<uint32_t *>(
             p.out + (static_cast<size_t>(row0 + r / p.group) * p.Hq +
