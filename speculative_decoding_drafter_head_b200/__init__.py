@@ -28,7 +28,7 @@ import os
 from . import _build
 
 __all__ = [
-    "DSparkError", "load", "workspace_bytes", "draft_step", "draft_step_rnn",
+    "DSparkError", "load", "calls", "workspace_bytes", "draft_step", "draft_step_rnn",
     "draft_confidence_step", "step", "confidence_sts", "schedule_prefix",
     "verify_prefix", "verify_layout", "qk_norm_rope_store", "verify_attention_workspace_bytes",
     "verify_attention", "sts_fit_workspace_bytes", "sts_fit", "get_error", "status_string", "set_wait_timeout_ns", "debug_barrier_extra",
@@ -52,6 +52,7 @@ EXPORTED = (
 )
 
 _lib = None
+_calls = None
 
 
 class DSparkError(RuntimeError):
@@ -248,36 +249,27 @@ def verify_prefix(x, L, target, accepted_out, bonus_out, stream=None):
     _check("dspark_verify_prefix", st)
 
 
-def _ptr(t, name, dtype, shape, device):
-    """The address of a tensor that a call of the verification pass can take as it is, else the
-    error that says why not.  One pass step makes these calls for every layer, so the checks
-    are few and cheap: 0.4 us a tensor."""
-    try:
-        if (t.dtype is dtype and t.shape == shape and t.is_contiguous() and
-                t.get_device() == device):
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _dev(t, dtype, name)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+def calls(build_if_missing: bool = True):
+    """The extension module that checks torch tensors and makes the verification pass's calls
+    (built first if it is missing or stale)."""
+    global _calls
+    if _calls is None:
+        import importlib.machinery
+        import importlib.util
 
-
-def _dims(t, n, name):
-    if getattr(t, "ndim", None) != n:
-        raise ValueError(f"{name} must be a tensor of {n} dimensions")
-    return t.shape
-
-
-def _here(stream):
-    """Current device, and the raw stream to launch on."""
-    import torch
-    torch.cuda._lazy_init()
-    device = torch._C._cuda_getDevice()
-    if stream is None:
-        return device, torch._C._cuda_getCurrentRawStream(device)
-    return device, stream.cuda_stream
+        import torch  # noqa: F401  (the module's symbols are torch's)
+        lib = load(build_if_missing)
+        if build_if_missing and _build.calls_stale():
+            _build.build_calls()
+        loader = importlib.machinery.ExtensionFileLoader("_dspark_calls", _build.CALLS)
+        mod = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("_dspark_calls", loader))
+        loader.exec_module(mod)
+        mod.bind(*(C.cast(f, C.c_void_p).value
+                   for f in (lib.dspark_verify_layout, lib.dspark_qk_norm_rope_store,
+                             lib.dspark_verify_attention)))
+        _calls = mod
+    return _calls
 
 
 def verify_layout(L, context, rows, pages, held, free_pages, free_count, row_start, position, slot,
@@ -289,29 +281,10 @@ def verify_layout(L, context, rows, pages, held, free_pages, free_count, row_sta
     free_count [1]; row_start [B + 1]; position, slot, token [row_capacity]; anchor [B],
     x [B, gamma]: all int32.  L, context, rows, pages, held, free_pages and free_count are
     the cache's state, updated in place."""
-    from torch import int32 as i32
-    B, max_pages = _dims(pages, 2, "pages")
-    cap, = _dims(position, 1, "position")
-    num_pages, = _dims(free_pages, 1, "free_pages")
-    if (anchor is None) != (token is None) or (x is None) != (token is None):
-        raise ValueError("anchor, x and token go together")
-    for name, t in (("L", L), ("context", context)):
-        if not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-    dev, raw = _here(stream)
-    per = (B,)
-    st = load().dspark_verify_layout(
-        _ptr(L, "L", i32, per, dev),
-        None if token is None else _ptr(anchor, "anchor", i32, per, dev),
-        None if token is None else _ptr(x, "x", i32, (B, gamma), dev),
-        None if accepted is None else _ptr(accepted, "accepted", i32, per, dev),
-        _ptr(context, "context", i32, per, dev), _ptr(rows, "rows", i32, per, dev),
-        _ptr(pages, "pages", i32, (B, max_pages), dev), _ptr(held, "held", i32, per, dev),
-        _ptr(free_pages, "free_pages", i32, (num_pages,), dev),
-        _ptr(free_count, "free_count", i32, (1,), dev), B, gamma, page_size, max_pages, num_pages,
-        cap, _ptr(row_start, "row_start", i32, (B + 1,), dev),
-        _ptr(position, "position", i32, (cap,), dev), _ptr(slot, "slot", i32, (cap,), dev),
-        None if token is None else _ptr(token, "token", i32, (cap,), dev), raw)
+    st = (_calls or calls()).verify_layout(
+        L, context, rows, pages, held, free_pages, free_count, row_start, position, slot,
+        page_size, gamma, anchor, x, token, accepted,
+        None if stream is None else stream.cuda_stream)
     if st:
         _check("dspark_verify_layout", st)
 
@@ -325,27 +298,9 @@ def qk_norm_rope_store(qkv, position, slot, n_rows, q_out, k_cache, v_cache, q_w
     qkv [row_capacity, (Hq + 2 Hkv) D] bf16, rows may be strided; position, slot
     [row_capacity] int32; n_rows [1] int32; q_out [row_capacity, Hq, D]; caches [num_pages,
     Hkv, page_size, D]; weights [D] bf16; inv_freq [rot_dim / 2] fp32."""
-    from torch import bfloat16 as bf, float32 as f32, int32 as i32
-    cap, Hq, D = _dims(q_out, 3, "q_out")
-    num_pages, Hkv, page_size, _ = _dims(k_cache, 4, "k_cache")
-    _dims(qkv, 2, "qkv")
-    if not qkv.is_cuda or qkv.dtype is not bf:
-        raise TypeError("qkv must be a CUDA tensor of torch.bfloat16")
-    dev, raw = _here(stream)
-    width = (Hq + 2 * Hkv) * D
-    if qkv.shape != (cap, width) or qkv.stride(1) != 1 or qkv.get_device() != dev:
-        raise ValueError(f"qkv must be [{cap}, {width}] on cuda:{dev}, contiguous along its channels")
-    cache, w = (num_pages, Hkv, page_size, D), (D,)
-    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
-    st = load().dspark_qk_norm_rope_store(
-        qkv.data_ptr(), qkv.stride(0) if cap > 1 else width,
-        None if q_weight is None else _ptr(q_weight, "q_weight", bf, w, dev),
-        None if k_weight is None else _ptr(k_weight, "k_weight", bf, w, dev), eps,
-        None if inv_freq is None else _ptr(inv_freq, "inv_freq", f32, (rot // 2,), dev), rot,
-        1 if interleaved else 0, rope_scale, _ptr(position, "position", i32, (cap,), dev),
-        _ptr(slot, "slot", i32, (cap,), dev), _ptr(n_rows, "n_rows", i32, (1,), dev), cap, Hq, Hkv,
-        D, page_size, num_pages, _ptr(q_out, "q_out", bf, (cap, Hq, D), dev),
-        _ptr(k_cache, "k_cache", bf, cache, dev), _ptr(v_cache, "v_cache", bf, cache, dev), raw)
+    st = (_calls or calls()).qk_norm_rope_store(
+        qkv, position, slot, n_rows, q_out, k_cache, v_cache, q_weight, k_weight, eps, inv_freq,
+        interleaved, rope_scale, None if stream is None else stream.cuda_stream)
     if st:
         _check("dspark_qk_norm_rope_store", st)
 
@@ -361,22 +316,10 @@ def verify_attention(q, k_cache, v_cache, pages, context, row_start, out, worksp
 
     q, out [row_capacity, Hq, D]; caches [num_pages, Hkv, page_size, D] bf16; pages
     [B, max_pages], context [B], row_start [B + 1] int32.  scale defaults to D ** -0.5."""
-    from torch import bfloat16 as bf, int32 as i32, uint8
-    cap, Hq, D = _dims(q, 3, "q")
-    num_pages, Hkv, page_size, _ = _dims(k_cache, 4, "k_cache")
-    B, max_pages = _dims(pages, 2, "pages")
-    size, = _dims(workspace, 1, "workspace")
-    if not q.is_cuda:
-        raise TypeError("q must be a CUDA tensor")
-    dev, raw = _here(stream)
-    rows, cache = (cap, Hq, D), (num_pages, Hkv, page_size, D)
-    st = load().dspark_verify_attention(
-        _ptr(q, "q", bf, rows, dev), _ptr(k_cache, "k_cache", bf, cache, dev),
-        _ptr(v_cache, "v_cache", bf, cache, dev), _ptr(pages, "pages", i32, (B, max_pages), dev),
-        _ptr(context, "context", i32, (B,), dev), _ptr(row_start, "row_start", i32, (B + 1,), dev),
-        B, cap, Hq, Hkv, D, page_size, max_pages, num_pages,
-        D ** -0.5 if scale is None else scale, _ptr(out, "out", bf, rows, dev),
-        _ptr(workspace, "workspace", uint8, (size,), dev), size, raw)
+    st = (_calls or calls()).verify_attention(
+        q, k_cache, v_cache, pages, context, row_start, out, workspace,
+        q.shape[-1] ** -0.5 if scale is None else scale,
+        None if stream is None else stream.cuda_stream)
     if st:
         _check("dspark_verify_attention", st)
 

@@ -1,4 +1,5 @@
-"""Build the CUDA library ``libdspark.so`` in-tree with nvcc for sm_100a."""
+"""Build the CUDA library ``libdspark.so`` in-tree with nvcc for sm_100a, and the extension
+module through which Python makes the verification pass's calls."""
 from __future__ import annotations
 
 import glob
@@ -10,6 +11,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libdspark.so")
+CALLS = os.path.join(PKG, "_dspark_calls.so")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
@@ -33,11 +35,47 @@ def _sources():
                   [os.path.join(ROOT, "include", "dspark.h")])
 
 
-def stale() -> bool:
-    if not os.path.exists(LIB):
+def _older(path, sources) -> bool:
+    if not os.path.exists(path):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(s) > t for s in _sources())
+    t = os.path.getmtime(path)
+    return any(os.path.getmtime(s) > t for s in sources)
+
+
+def _calls_sources():
+    return [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "dspark.h")]
+
+
+def stale() -> bool:
+    return _older(LIB, _sources())
+
+
+def calls_stale() -> bool:
+    return _older(CALLS, _calls_sources())
+
+
+def build_calls(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/binding.cpp against this interpreter and its torch."""
+    if not force and not calls_stale():
+        return CALLS
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    tmp = CALLS + f".tmp{os.getpid()}"
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    include = [*cpp_extension.include_paths(), os.path.join(cuda, "include"),
+               sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-isystem{i}" for i in include], "-o", tmp, os.path.join(CSRC, "binding.cpp"),
+           f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.check_call(cmd)
+    os.replace(tmp, CALLS)
+    return CALLS
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -56,3 +94,4 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 if __name__ == "__main__":
     print(build(force=True, verbose=True))
+    print(build_calls(force=True, verbose=True))

@@ -698,18 +698,22 @@ int dspark_verify_layout(int32_t *L, const int32_t *anchor, const int32_t *x,
     prm.slot = slot;
     prm.token = token;
     const size_t smem = static_cast<size_t>(B) * Y::kWordsPerRequest * 4;
+    const bool few = B <= Y::kThreadsFew;
+    void (*kern)(const Y::Params) = few ? Y::verify_layout_kernel<Y::kThreadsFew>
+                                        : Y::verify_layout_kernel<Y::kThreadsMany>;
     if (smem > 40 * 1024 &&
-        cudaFuncSetAttribute(Y::verify_layout_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              Y::kMaxB * Y::kWordsPerRequest * 4) != cudaSuccess)
         return DSPARK_CUDA_ERROR;
-    // one CTA for the rows of up to one thread each, then more, up to a portable cluster
+    // CTAs for one row to a thread, up to a portable cluster
+    const int threads = few ? Y::kThreadsFew : Y::kThreadsMany;
     const long long most = static_cast<long long>(B) * (gamma + 1);
     int ctas = 1;
-    while (ctas < 8 && most > static_cast<long long>(ctas) * Y::kThreads) ctas *= 2;
+    while (ctas < 8 && most > static_cast<long long>(ctas) * threads) ctas *= 2;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(Y::kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -719,7 +723,7 @@ int dspark_verify_layout(int32_t *L, const int32_t *anchor, const int32_t *x,
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return from_cuda(cudaLaunchKernelEx(&cfg, Y::verify_layout_kernel, prm));
+    return from_cuda(cudaLaunchKernelEx(&cfg, kern, prm));
 }
 
 int dspark_qk_norm_rope_store(const void *qkv, int64_t qkv_stride, const void *q_weight,

@@ -24,8 +24,7 @@
 namespace dspark {
 namespace layout {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreadsFew = 128, kThreadsMany = 1024;   // to a CTA, for up to 128 requests or more
 constexpr int kMaxB = 4096;
 constexpr int kWordsPerRequest = 6;
 
@@ -44,6 +43,7 @@ struct Params {
 };
 
 // Exclusive running sum of one 64-bit value per thread; `total` is the sum of all.
+template <int kThreads>
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long v,
                                                          unsigned long long *warp_sums,
                                                          unsigned long long &total)
@@ -61,7 +61,7 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v,
     unsigned long long before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         const unsigned long long t = warp_sums[w];
         if (w < warp) before += t;
         total += t;
@@ -79,8 +79,10 @@ __device__ __forceinline__ int checked_length(int v, int lo, int hi)
     return v;
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) verify_layout_kernel(const Params p)
 {
+    constexpr int kWarps = kThreads / 32;
     extern __shared__ int32_t words[];
     __shared__ unsigned long long warp_sums[kWarps];
     int32_t *s_ctx = words, *s_want = words + p.B, *s_held = words + 2 * p.B;
@@ -90,22 +92,26 @@ __global__ void __launch_bounds__(kThreads) verify_layout_kernel(const Params p)
     const int room = static_cast<int>(
         min(static_cast<long long>(p.max_pages) * p.ps, static_cast<long long>(INT32_MAX)));
 
-    const int F = checked_length(*p.free_count, 0, p.num_pages);
+    const int free_count = *p.free_count;         // used after the first sums
     unsigned long long carry = 0;                 // pages returned << 32 | pages asked for
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         const int b = b0 + tid;
         int back = 0, ask = 0, ctx = -1, want = 0, held = 0;
         if (b < p.B) {
+            // all loads first: none waits for another's value
             ctx = p.context[b];
-            if (p.accepted && ctx >= 0) {
-                const int grown = min(checked_length(p.accepted[b], -1, INT32_MAX - 1) + 1,
-                                      max(p.rows[b], 0));
+            const int len = p.L[b], had = p.held[b];
+            const int accepted = p.accepted ? p.accepted[b] : -1;
+            const int sent_before = p.accepted ? p.rows[b] : 0;
+            if (ctx >= 0) {
+                const int grown = min(checked_length(accepted, -1, INT32_MAX - 1) + 1,
+                                      max(sent_before, 0));
                 ctx = static_cast<int>(min(static_cast<long long>(ctx) + grown,
                                            static_cast<long long>(INT32_MAX)));
             }
             ctx = checked_length(ctx, -1, room);
-            if (ctx >= 0) want = checked_length(p.L[b], 0, p.gamma) + 1;
-            held = checked_length(p.held[b], 0, p.max_pages);
+            if (ctx >= 0) want = checked_length(len, 0, p.gamma) + 1;
+            held = checked_length(had, 0, p.max_pages);
             const int sent = min(want, room - max(ctx, 0));   // what the block table has room for
             const int need = ctx < 0 ? 0 : static_cast<int>((static_cast<long long>(ctx) + sent +
                                                              p.ps - 1) / p.ps);
@@ -115,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) verify_layout_kernel(const Params p)
         }
         unsigned long long total;
         const unsigned long long at =
-            carry + block_scan(static_cast<unsigned long long>(back) << 32 |
+            carry + block_scan<kThreads>(static_cast<unsigned long long>(back) << 32 |
                                    static_cast<unsigned>(ask), warp_sums, total);
         carry += total;
         if (b < p.B) {
@@ -126,6 +132,7 @@ __global__ void __launch_bounds__(kThreads) verify_layout_kernel(const Params p)
             s_ask[b] = static_cast<int>(at);
         }
     }
+    const int F = checked_length(free_count, 0, p.num_pages);
     const int returned = static_cast<int>(carry >> 32);
     const unsigned asked = static_cast<unsigned>(carry);
     // the stack after the returns; pages past the array's end (a caller's page that stands
@@ -154,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) verify_layout_kernel(const Params p)
         }
         unsigned long long total;
         const unsigned long long at =
-            rows_before + block_scan(static_cast<unsigned>(n), warp_sums, total);
+            rows_before + block_scan<kThreads>(static_cast<unsigned>(n), warp_sums, total);
         rows_before += total;
         if (b < p.B) s_row[b] = static_cast<int>(at);
     }
