@@ -55,6 +55,7 @@ struct DeviceInfo {
     // context with this id (0: none yet); a new context (after a device reset) re-sets them
     unsigned long long draft_ctx = 0;
     int pair_clusters = 0;
+    unsigned long long attention_ctx = 0;   // the same for the verification's attention kernels
 };
 
 using CtxGetCurrentFn = CUresult (*)(CUcontext *);
@@ -864,8 +865,26 @@ int dspark_verify_attention(const void *q, const void *k_cache, const void *v_ca
                 : (wide ? A::verify_attention_kernel<128, A::kMaxRows> : A::verify_attention_kernel<128, 64>);
     const int smem = D == 64 ? (wide ? A::smem_bytes<64, A::kMaxRows>() : A::smem_bytes<64, 64>())
                              : (wide ? A::smem_bytes<128, A::kMaxRows>() : A::smem_bytes<128, 64>());
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return DSPARK_CUDA_ERROR;
+    {
+        const unsigned long long ctx = current_ctx_id();
+        std::lock_guard<std::mutex> lock(g_dev_mutex);
+        if (ctx == 0 || dev->attention_ctx != ctx) {
+            const struct {
+                void (*kern)(const CUtensorMap, const CUtensorMap, const A::Params);
+                int smem;
+            } all[] = {{A::verify_attention_kernel<64, 64>, A::smem_bytes<64, 64>()},
+                       {A::verify_attention_kernel<64, A::kMaxRows>,
+                        A::smem_bytes<64, A::kMaxRows>()},
+                       {A::verify_attention_kernel<128, 64>, A::smem_bytes<128, 64>()},
+                       {A::verify_attention_kernel<128, A::kMaxRows>,
+                        A::smem_bytes<128, A::kMaxRows>()}};
+            for (const auto &k : all)
+                if (cudaFuncSetAttribute(k.kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         k.smem) != cudaSuccess)
+                    return DSPARK_CUDA_ERROR;
+            dev->attention_ctx = ctx;
+        }
+    }
     const int grid = dev->sms < A::kMaxCtas ? dev->sms : A::kMaxCtas;
     kern<<<grid, A::kThreads, smem, stream>>>(tm_k, tm_v, prm);
     if (cudaGetLastError() != cudaSuccess) return DSPARK_CUDA_ERROR;

@@ -447,6 +447,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (t1 > t0 && before <= t0 && t0 < before + mine) {
         long long at = before;
         for (int r = r0; r < min(r0 + per, p.B); ++r) {
+            if (r + 1 == min(r0 + per, p.B)) {    // the last one it can be
+                ctl.start_b = r;
+                ctl.start_off = t0 - at;
+                break;
+            }
             int ctx, rows, start;
             bool bad;
             load_request(p, r, ctx, rows, start, bad);

@@ -23,6 +23,14 @@ namespace vplan {
 constexpr int kTileKeys = 128;
 constexpr int kUnitCost = 3;
 
+// a / b, both at least 0: a 64-bit division takes the device several times a 32-bit one's time,
+// and the kernel's first copies wait for these
+DSPARK_HD long long quotient(long long a, long long b)
+{
+    if ((a | b) >> 31 == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    return a / b;
+}
+
 // sum over i = 0 .. n - 1 of floor((a i + b) / 2^7), a, b >= 0, by Euclid's steps
 DSPARK_HD long long floor_sum(long long n, long long a, long long b)
 {
@@ -73,11 +81,11 @@ struct Request {
 };
 
 // first place of CTA c of G
-DSPARK_HD long long first_place(long long T, int c, int G) { return T * c / G; }
+DSPARK_HD long long first_place(long long T, int c, int G) { return quotient(T * c, G); }
 // the CTA that holds place t
 DSPARK_HD int cta_of(long long T, long long t, int G)
 {
-    return static_cast<int>(((t + 1) * G - 1) / T);
+    return static_cast<int>(quotient((t + 1) * G - 1, T));
 }
 // CTAs that take part: each has at least one place
 DSPARK_HD int ctas(long long T, int most) { return T < most ? static_cast<int>(T) : most; }
@@ -86,7 +94,7 @@ DSPARK_HD int ctas(long long T, int most) { return T < most ? static_cast<int>(T
 DSPARK_HD void place(const Request &r, long long at, int &h, int &qt, int &in_unit)
 {
     const long long per = r.per_head();
-    h = static_cast<int>(at / per);
+    h = static_cast<int>(quotient(at, per));
     const long long rest = at - h * per;
     int lo = 0, hi = r.query_tiles() - 1;
     while (lo < hi) {
