@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     long long T = 0, before = 0;
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += ctl.sums[w];
         T += ctl.sums[w];

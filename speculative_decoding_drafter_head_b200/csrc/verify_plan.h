@@ -13,8 +13,10 @@
 
 #ifdef __CUDACC__
 #define DSPARK_HD __host__ __device__ __forceinline__
+#define DSPARK_HD_CALL __host__ __device__ __noinline__
 #else
 #define DSPARK_HD inline
+#define DSPARK_HD_CALL inline
 #endif
 
 namespace dspark {
@@ -32,7 +34,9 @@ DSPARK_HD long long quotient(long long a, long long b)
 }
 
 // sum over i = 0 .. n - 1 of floor((a i + b) / 2^7), a, b >= 0, by Euclid's steps
-DSPARK_HD long long floor_sum(long long n, long long a, long long b)
+// (a call: only requests of three query tiles or more come here, and inlined where it is used it
+// is most of what a CTA fetches as instructions before its first copy)
+DSPARK_HD_CALL long long floor_sum(long long n, long long a, long long b)
 {
     long long m = kTileKeys, sum = 0;
     while (true) {
