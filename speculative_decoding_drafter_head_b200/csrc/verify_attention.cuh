@@ -156,19 +156,25 @@ __device__ __forceinline__ void load_request(const Params &p, int b, int &ctx, i
     }
 }
 
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Ctl &ctl, const Params &p)
+// A wait that does not succeed at once; a call, to keep the loops that make it short.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, int *abort,
+                                       unsigned long long timeout_ns)
 {
-    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
         if (mbar_try_wait_sleep(bar, parity, kWaitHintNs)) return true;
-        if (*reinterpret_cast<volatile int *>(&ctl.abort)) return false;
-        if (globaltimer_ns() - t0 > p.timeout_ns) {
+        if (*reinterpret_cast<volatile int *>(abort)) return false;
+        if (globaltimer_ns() - t0 > timeout_ns) {
             record_error(DSPARK_TIMEOUT);
-            *reinterpret_cast<volatile int *>(&ctl.abort) = 1;
+            *reinterpret_cast<volatile int *>(abort) = 1;
             return false;
         }
     }
+}
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, Ctl &ctl, const Params &p)
+{
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, &ctl.abort, p.timeout_ns);
 }
 
 // The same for a whole warp, which goes on only if every lane may.
