@@ -559,68 +559,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         // One thread, from start to end: votes and walks of a whole warp took longer than the
         // MMAs themselves (800 of 1900 cycles a tile with D = 64).
         if (elect_one()) {
-            const uint64_t ones = smem_desc(s0 + C::kOnes, 128, 128, kSwizzleNone);
+            // descriptors: high halves, and low halves of the first buffers
             const uint64_t dk = smem_desc(s0 + C::kRing, 16, 1024, kSwizzle128B);
             const uint64_t dv = smem_desc(s0 + C::kRingV, C::kHalfBytes, 1024, kSwizzle128B);
-            const uint64_t dq = smem_desc(s0 + C::kQ, 16, 1024, kSwizzle128B);
             const uint64_t dp = smem_desc(s0 + C::kP, kTileKeys * 128, 1024, kSwizzle128B);
-            uint32_t i = 0, seg = 0;
-            // the tile whose values are to be added: its columns, its segment, first or last of it
-            uint32_t pn = 0, pseg = 0;
-            bool pfirst = false, plast = false, ok = true;
+            const uint64_t d1 = smem_desc(s0 + C::kOnes, 128, 128, kSwizzleNone);
+            const uint32_t k_hi = dk >> 32, v_hi = dv >> 32, p_hi = dp >> 32, ones_hi = d1 >> 32;
+            const uint32_t k_lo = dk, v_lo = dv, p_lo = dp, ones_lo = d1;
+            const uint32_t q_lo = k_lo + ((C::kQ - C::kRing) >> 4);
+            // ring slot and phase, parity of the tile, for S and, a tile later, for O
+            uint32_t slot = 0, phase = 0, odd = 0, pslot = 0, pphase = 0, podd = 0, pturn = 0;
+            uint32_t pid_o = 0, pid_l = 0, seg = 0;
+            bool pfirst = false, plast = false, ok = true, any = false;
             auto values = [&]() {
-                const uint32_t j = i - 1, slot = j % C::kSlots, ob = pseg % C::kOBufs;
-                ok = wait(v_full + 8 * slot, (j / C::kSlots) & 1u, ctl, p) &&
+                const uint32_t ob = seg % C::kOBufs;   // of the tile's segment: see below
+                ok = wait(v_full + 8 * pslot, pphase, ctl, p) &&
                      (!pfirst ||
-                      wait(o_empty + 8 * ob, ((pseg / C::kOBufs) & 1u) ^ 1u, ctl, p)) &&
-                     wait(p_full + 8 * (j & 1), (j >> 1) & 1u, ctl, p);
+                      wait(o_empty + 8 * ob, ((seg / C::kOBufs) & 1u) ^ 1u, ctl, p)) &&
+                     wait(p_full + 8 * podd, pturn, ctl, p);
                 if (!ok) return;
                 tc_fence_after();
-                const uint64_t a = dv + slot * (C::kTileBytes >> 4);
-                const uint64_t b = dp + (j & 1) * (C::kPBytes >> 4);
+                const uint32_t a = v_lo + pslot * (C::kTileBytes >> 4);
+                const uint32_t b = p_lo + podd * (C::kPBytes >> 4);
                 const uint32_t to = tmem + C::kColO + ob * kN, tl = tmem + C::kColL + ob * kN;
-                const uint32_t id_o = idesc_bf16_f32(D, pn, 1, 1);
-                const uint32_t id_l = idesc_bf16_f32(64, pn, 0, 1);
 #pragma unroll
                 for (int k = 0; k < kTileKeys / 16; ++k) {
-                    const uint32_t acc = !pfirst || k > 0;
-                    umma_bf16(to, a + k * 128, b + k * 128, id_o, acc);
-                    umma_bf16(tl, ones, b + k * 128, id_l, acc);
+                    const bool acc = k > 0 || !pfirst;
+                    umma_bf16(to, a + k * 128, v_hi, b + k * 128, p_hi, pid_o, acc);
+                    umma_bf16(tl, ones_lo, ones_hi, b + k * 128, p_hi, pid_l, acc);
                 }
-                umma_commit(o_done + 8 * slot);
+                umma_commit(o_done + 8 * pslot);
                 if (plast) umma_commit(o_full + 8 * ob);
+                if (++pslot == C::kSlots) pslot = 0, pphase ^= 1u;
+                podd ^= 1u;
+                if (podd == 0) pturn ^= 1u;
             };
-            for (; ok; ++seg) {
-                const uint32_t qb = seg % C::kQBufs;
-                if (!wait(q_full + 8 * qb, (seg / C::kQBufs) & 1u, ctl, p)) ok = false;
+            for (uint32_t next = 0; ok; ++next) {
+                // segment `next`; `seg` stays the one of the tile whose values are to be added
+                const uint32_t qb = next % C::kQBufs;
+                if (!wait(q_full + 8 * qb, (next / C::kQBufs) & 1u, ctl, p)) ok = false;
                 if (!ok) break;
                 const uint32_t n = ctl.seg_n[qb];
                 const int tiles = ctl.seg_tiles[qb];
                 if (tiles == 0) break;
                 const uint32_t id = idesc_bf16_f32(kTileKeys, n, 0, 0);
-                const uint64_t b = dq + qb * (C::kQBytes >> 4);
+                const uint32_t q = q_lo + qb * (C::kQBytes >> 4);
                 for (int t = 0; t < tiles; ++t) {
-                    const uint32_t slot = i % C::kSlots;
-                    if (!wait(k_full + 8 * slot, (i / C::kSlots) & 1u, ctl, p)) {
+                    if (!wait(k_full + 8 * slot, phase, ctl, p)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t a = dk + slot * (C::kTileBytes >> 4);
+                    const uint32_t a = k_lo + slot * (C::kTileBytes >> 4);
+                    const uint32_t to = tmem + C::kColS + odd * kN;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        umma_bf16(tmem + C::kColS + (i & 1) * kN,
-                                  a + (k >> 2) * (C::kHalfBytes >> 4) + (k & 3) * 2,
-                                  b + (k >> 2) * (kN * 128 >> 4) + (k & 3) * 2, id, k > 0);
+                        umma_bf16(to, a + (k >> 2) * (C::kHalfBytes >> 4) + (k & 3) * 2, k_hi,
+                                  q + (k >> 2) * (kN * 128 >> 4) + (k & 3) * 2, k_hi, id, k > 0);
                     umma_commit(s_full + 8 * slot);
                     if (t + 1 == tiles) umma_commit(q_empty + 8 * qb);
-                    if (i > 0) values();
+                    if (++slot == C::kSlots) slot = 0, phase ^= 1u;
+                    odd ^= 1u;
+                    if (any) values();
                     if (!ok) break;
-                    pn = n, pseg = seg, pfirst = t == 0, plast = t + 1 == tiles;
-                    ++i;
+                    any = true;
+                    seg = next;
+                    pfirst = t == 0, plast = t + 1 == tiles;
+                    pid_o = idesc_bf16_f32(D, n, 1, 1);
+                    pid_l = idesc_bf16_f32(64, n, 0, 1);
                 }
             }
-            if (ok && i > 0) values();
+            if (ok && any) values();
             umma_commit(drain);                   // MMAs finish before the CTA ends
             wait_drain(drain, 0, p);
         }
