@@ -96,6 +96,8 @@ template <int D, int kN>
 struct Cfg {
     static constexpr int kQBufs = kN == 64 ? 2 : 1;
     static constexpr int kOBufs = kN == 64 ? 2 : 1;
+    static constexpr int kPBufs = kN == 64 ? 3 : 2;
+    static constexpr int kMBufs = kN == 64 ? 8 : 4;          // references m, by segment
     static constexpr int kTileBytes = kTileKeys * D * 2;
     static constexpr int kHalfBytes = kTileKeys * 128;       // 64 channels of a tile
     static constexpr int kSlots = 2 * (128 / D);             // K tiles, and V tiles, in the ring
@@ -105,29 +107,40 @@ struct Cfg {
     static constexpr int kRingV = kRing + kSlots * kTileBytes;
     static constexpr int kQ = kRingV + kSlots * kTileBytes;
     static constexpr int kP = kQ + kQBufs * kQBytes;
-    static constexpr int kOnes = kP + 2 * kPBytes;
-    static constexpr int kM = kOnes + kOnesBytes;            // float [2][kN]
-    static constexpr int kRed = kM + 2 * kN * 4;             // float [2 groups][4][kN]
+    static constexpr int kOnes = kP + kPBufs * kPBytes;
+    static constexpr int kM = kOnes + kOnesBytes;            // float [kMBufs][kN]
+    static constexpr int kRed = kM + kMBufs * kN * 4;             // float [2 groups][4][kN]
     static constexpr int kCtl = kRed + 2 * 4 * kN * 4;
     static constexpr uint32_t kColS = 0, kColO = 2 * kN, kColL = kColO + kOBufs * kN;
     static_assert(kColL + kOBufs * kN <= kTmemCols, "tensor memory");
 };
 
-constexpr int kMaxSlots = 4;
+// Barriers of the tiles, four of a kind whatever the ring's depth.  A wait by parity cannot tell a
+// phase from the one two back or two ahead, so nobody may wait for a tile's phase while the
+// fourth tile before it is still open or once the fourth after it is done.  Who has seen S of
+// tile i knows that the values of tile i - 3 have been added, and S and O of tile i + 4 need
+// the weights of tile i + 2, of the same softmax group: waits for tiles i - 4 to i are safe.
+constexpr uint32_t kTileBars = 4;
+__device__ __forceinline__ uint32_t tile_bar(uint32_t bars, uint32_t t)
+{
+    return bars + 8 * (t % kTileBars);
+}
+__device__ __forceinline__ uint32_t tile_phase(uint32_t t) { return t / kTileBars & 1u; }
+
 constexpr int kMaxBoxes = kTileKeys / 16;         // pages of a tile at most
 
 struct Ctl {
-    // by ring slot: K copied, V copied, S made (and K's slot free), O added to (and V's slot free)
-    unsigned long long k_full[kMaxSlots], v_full[kMaxSlots], s_full[kMaxSlots], o_done[kMaxSlots];
+    // by tile: K copied, V copied, S made (and K's slot free), O added to (and V's slot free)
+    unsigned long long k_full[kTileBars], v_full[kTileBars], s_full[kTileBars], o_done[kTileBars];
     unsigned long long p_full[2], m_full[2];
-    unsigned long long q_full[2], q_empty[2], o_full[2], o_empty[2], drain;
+    unsigned long long q_full[2], q_empty[2], o_empty[2], drain;
     long long start_off;                          // first place in its request
     unsigned long long sums[kThreads / 32];
     int start_b;
     uint32_t tmem;
     int abort;
     int epoch;                                    // times that a reference m rose
-    int odd[2];                                   // a cleared value, by parity of the segment
+    int odd[8];                                   // a cleared value, by segment as for m
     int seg_n[2], seg_tiles[2];                   // the segment of a Q buffer; no tiles: the end
 };
 
@@ -411,10 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_full = smem_u32(ctl.s_full), o_done = smem_u32(ctl.o_done);
     const uint32_t p_full = smem_u32(ctl.p_full), m_full = smem_u32(ctl.m_full);
     const uint32_t q_full = smem_u32(ctl.q_full);
-    const uint32_t q_empty = smem_u32(ctl.q_empty), o_full = smem_u32(ctl.o_full);
+    const uint32_t q_empty = smem_u32(ctl.q_empty);
     const uint32_t o_empty = smem_u32(ctl.o_empty), drain = smem_u32(&ctl.drain);
     if (tid == 0) {
-        for (int i = 0; i < C::kSlots; ++i) {
+        for (uint32_t i = 0; i < kTileBars; ++i) {
             mbar_init(k_full + 8 * i, 1);
             mbar_init(v_full + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
@@ -425,14 +438,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(m_full + 8 * i, kSoftThreads);
             mbar_init(q_full + 8 * i, kQThreads);
             mbar_init(q_empty + 8 * i, 1);
-            mbar_init(o_full + 8 * i, 1);
             mbar_init(o_empty + 8 * i, kSoftThreads);
         }
         mbar_init(drain, 1);
         mbar_fence_init();
         ctl.abort = 0;
         ctl.epoch = 0;
-        ctl.odd[0] = ctl.odd[1] = 0;
+        for (int i = 0; i < 8; ++i) ctl.odd[i] = 0;
     }
     if (warp == kWarpMma) {
         tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
@@ -532,10 +544,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < kMaxBoxes; ++j) row[j] = __shfl_sync(0xFFFFFFFFu, id, j);
                 const uint32_t slot = i % C::kSlots;
-                ok = warp_wait(empty + 8 * slot, ((i / C::kSlots) & 1u) ^ 1u, ctl, p);
+                if (i >= C::kSlots)
+                    ok = warp_wait(tile_bar(empty, i - C::kSlots), tile_phase(i - C::kSlots), ctl, p);
                 if (!ok) break;
                 if (elect_one()) {
-                    const uint32_t bar = full + 8 * slot;
+                    const uint32_t bar = tile_bar(full, i);
                     uint32_t dst = ring + slot * C::kTileBytes;
                     mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n) * p.ps * D * 2);
 #pragma unroll
@@ -553,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // copies land before the CTA ends
         for (uint32_t back = 1; back <= C::kSlots && back <= i; ++back)
-            wait_drain(full + 8 * ((i - back) % C::kSlots), ((i - back) / C::kSlots) & 1u, p);
+            wait_drain(tile_bar(full, i - back), tile_phase(i - back), p);
     } else if (warp == kWarpMma) {
         // ---------------------------------------------------- S^T = K Q^T, O^T += V^T P
         // One thread, from start to end: votes and walks of a whole warp took longer than the
@@ -567,37 +580,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t k_hi = dk >> 32, v_hi = dv >> 32, p_hi = dp >> 32, ones_hi = d1 >> 32;
             const uint32_t k_lo = dk, v_lo = dv, p_lo = dp, ones_lo = d1;
             const uint32_t q_lo = k_lo + ((C::kQ - C::kRing) >> 4);
-            // ring slot and phase, parity of the tile, for S and, a tile later, for O
-            uint32_t slot = 0, phase = 0, odd = 0, pslot = 0, pphase = 0, podd = 0, pturn = 0;
-            uint32_t pid_o = 0, pid_l = 0, seg = 0;
-            bool pfirst = false, plast = false, ok = true, any = false;
+            // S runs two tiles ahead of O: once the weights of tile i are there, S of tile i + 2
+            // goes first, since its softmax waits for it, and the values of tile i after it; or
+            // the other way round while keys or queries are still on their way.
+            struct Tile {
+                uint32_t id_o, id_l, seg;
+                bool first;                       // of its segment
+            } t0 = {}, t1 = {};
+            uint32_t ahead = 0;                   // tiles in t0, t1
+            // tile, ring slot and P buffer: of the next S, and of the next values
+            uint32_t i = 0, slot = 0, j = 0, jslot = 0, jbuf = 0;
+            bool ok = true;
+            auto weights_there = [&]() { return wait(p_full + 8 * (j & 1), (j >> 1) & 1u, ctl, p); };
             auto values = [&]() {
-                const uint32_t ob = seg % C::kOBufs;   // of the tile's segment: see below
-                ok = wait(v_full + 8 * pslot, pphase, ctl, p) &&
-                     (!pfirst ||
-                      wait(o_empty + 8 * ob, ((seg / C::kOBufs) & 1u) ^ 1u, ctl, p)) &&
-                     wait(p_full + 8 * podd, pturn, ctl, p);
+                const uint32_t ob = t0.seg % C::kOBufs;
+                ok = wait(tile_bar(v_full, j), tile_phase(j), ctl, p) &&
+                     (!t0.first ||
+                      wait(o_empty + 8 * ob, ((t0.seg / C::kOBufs) & 1u) ^ 1u, ctl, p));
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t a = v_lo + pslot * (C::kTileBytes >> 4);
-                const uint32_t b = p_lo + podd * (C::kPBytes >> 4);
+                const uint32_t a = v_lo + jslot * (C::kTileBytes >> 4);
+                const uint32_t b = p_lo + jbuf * (C::kPBytes >> 4);
                 const uint32_t to = tmem + C::kColO + ob * kN, tl = tmem + C::kColL + ob * kN;
 #pragma unroll
                 for (int k = 0; k < kTileKeys / 16; ++k) {
-                    const bool acc = k > 0 || !pfirst;
-                    umma_bf16(to, a + k * 128, v_hi, b + k * 128, p_hi, pid_o, acc);
-                    umma_bf16(tl, ones_lo, ones_hi, b + k * 128, p_hi, pid_l, acc);
+                    const bool acc = k > 0 || !t0.first;
+                    umma_bf16(to, a + k * 128, v_hi, b + k * 128, p_hi, t0.id_o, acc);
+                    umma_bf16(tl, ones_lo, ones_hi, b + k * 128, p_hi, t0.id_l, acc);
                 }
-                umma_commit(o_done + 8 * pslot);
-                if (plast) umma_commit(o_full + 8 * ob);
-                if (++pslot == C::kSlots) pslot = 0, pphase ^= 1u;
-                podd ^= 1u;
-                if (podd == 0) pturn ^= 1u;
+                umma_commit(tile_bar(o_done, j));
+                ++j;
+                if (++jslot == C::kSlots) jslot = 0;
+                if (++jbuf == C::kPBufs) jbuf = 0;
+                t0 = t1;
+                --ahead;
             };
-            for (uint32_t next = 0; ok; ++next) {
-                // segment `next`; `seg` stays the one of the tile whose values are to be added
-                const uint32_t qb = next % C::kQBufs;
-                if (!wait(q_full + 8 * qb, (next / C::kQBufs) & 1u, ctl, p)) ok = false;
+            for (uint32_t seg = 0; ok; ++seg) {
+                const uint32_t qb = seg % C::kQBufs;
+                const uint32_t turn = (seg / C::kQBufs) & 1u;
+                while (ok && ahead > 0 && !mbar_test_wait(q_full + 8 * qb, turn)) {
+                    ok = weights_there();
+                    if (ok) values();
+                }
+                ok = ok && wait(q_full + 8 * qb, turn, ctl, p);
                 if (!ok) break;
                 const uint32_t n = ctl.seg_n[qb];
                 const int tiles = ctl.seg_tiles[qb];
@@ -605,31 +630,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t id = idesc_bf16_f32(kTileKeys, n, 0, 0);
                 const uint32_t q = q_lo + qb * (C::kQBytes >> 4);
                 for (int t = 0; t < tiles; ++t) {
-                    if (!wait(k_full + 8 * slot, phase, ctl, p)) {
-                        ok = false;
-                        break;
+                    if (ahead == 2) {             // S's buffer is free once they are
+                        ok = weights_there();
+                        if (ok && !mbar_test_wait(tile_bar(k_full, i), tile_phase(i))) values();
                     }
+                    ok = ok && wait(tile_bar(k_full, i), tile_phase(i), ctl, p);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t a = k_lo + slot * (C::kTileBytes >> 4);
-                    const uint32_t to = tmem + C::kColS + odd * kN;
+                    const uint32_t to = tmem + C::kColS + (i & 1) * kN;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         umma_bf16(to, a + (k >> 2) * (C::kHalfBytes >> 4) + (k & 3) * 2, k_hi,
                                   q + (k >> 2) * (kN * 128 >> 4) + (k & 3) * 2, k_hi, id, k > 0);
-                    umma_commit(s_full + 8 * slot);
+                    umma_commit(tile_bar(s_full, i));
                     if (t + 1 == tiles) umma_commit(q_empty + 8 * qb);
-                    if (++slot == C::kSlots) slot = 0, phase ^= 1u;
-                    odd ^= 1u;
-                    if (any) values();
+                    ++i;
+                    if (++slot == C::kSlots) slot = 0;
+                    if (ahead == 2) values();
                     if (!ok) break;
-                    any = true;
-                    seg = next;
-                    pfirst = t == 0, plast = t + 1 == tiles;
-                    pid_o = idesc_bf16_f32(D, n, 1, 1);
-                    pid_l = idesc_bf16_f32(64, n, 0, 1);
+                    const Tile cur = {idesc_bf16_f32(D, n, 1, 1), idesc_bf16_f32(64, n, 0, 1), seg,
+                                      t == 0};
+                    if (ahead == 0) t0 = cur;
+                    else t1 = cur;
+                    ++ahead;
                 }
             }
-            if (ok && any) values();
+            while (ok && ahead > 0) {
+                ok = weights_there();
+                if (ok) values();
+            }
             umma_commit(drain);                   // MMAs finish before the CTA ends
             wait_drain(drain, 0, p);
         }
@@ -687,7 +717,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         struct Seg {
             int row0, rows, h, kt, kt_end, keys, hidden, b;   // hidden: keys that row 0 sees
             bool starts, ends;
-        } cur = {};
+        } cur = {}, late = {};
+        bool owed = false;                        // the output of `late` is still to be written
+        uint32_t late_seg = 0, late_tile = 0;
         int4 desc = make_int4(0, 0, 0, 0);
 
         // after a wait that ran out the warps go on without waiting, so that they meet at the
@@ -696,16 +728,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto await = [&](uint32_t bar, uint32_t parity) {
             if (!dead && !wait(bar, parity, ctl, p)) dead = true;
         };
-
         // l, O -> out, or to the workspace when the unit has other parts
-        auto output = [&](const Seg &s, uint32_t seg) {
+        auto output = [&](const Seg &s, uint32_t seg, uint32_t last_tile) {
             const uint32_t ob = seg % C::kOBufs;
-            await(o_full + 8 * ob, (seg / C::kOBufs) & 1u);
+            await(tile_bar(o_done, last_tile), tile_phase(last_tile));
             __syncwarp();
             tc_fence_after();
             const bool direct = s.starts && s.ends;
             const int part = 2 * blockIdx.x + (s.starts ? 1 : 0);
-            const bool odd = *reinterpret_cast<volatile int *>(&ctl.odd[seg & 1]);
+            const bool odd = *reinterpret_cast<volatile int *>(&ctl.odd[seg % C::kMBufs]);
             // a thread per row: 1 / l and the row's place in the output, or (m, l)
             for (int c0 = 16 * quad; c0 < s.rows; c0 += 64) {
                 uint32_t l[16];
@@ -724,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     red[at] = 1.0f / l;
                 } else {
                     p.part_ml[static_cast<size_t>(part) * kMaxRows + at] =
-                        make_float2(m_s[(seg & 1) * kN + at], l);
+                        make_float2(m_s[seg % C::kMBufs * kN + at], l);
                 }
             }
             group_sync(wg);
@@ -781,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             group_sync(wg);                       // red is free again
-            if (at == 0) ctl.odd[seg & 1] = 0;
+            if (at == 0) ctl.odd[seg % C::kMBufs] = 0;
             tc_fence_before();
             mbar_arrive(o_empty + 8 * ob);
         };
@@ -827,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 desc = make_int4(cur.row0, cur.h, cur.rows,
                                  vplan::cta_of(T, t1 - 1 + (w.tiles - w.kt_end), G) - cta + 1);
             const int n = (cur.rows + 15) & ~15;
-            float *m_row = m_s + (seg & 1) * kN;
+            float *m_row = m_s + seg % C::kMBufs * kN;
             int kt = cur.kt + ((i & 1) == static_cast<uint32_t>(wg) ? 0 : 1);
             i += kt - cur.kt;
             for (; kt < cur.kt_end; kt += 2, i += 2) {
@@ -840,17 +871,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool masked = (kt + 1) * kTileKeys > cur.hidden;
                 const bool first = kt == cur.kt;
                 const uint32_t before = p_full + 8 * (wg ^ 1), before_phase = ((i - 1) >> 1) & 1u;
-                await(s_full + 8 * (i % C::kSlots), (i / C::kSlots) & 1u);
-                // m of this segment: to be set here, once the other group has left the tile
-                // before (and what it still read of older segments), or set by the other
+                await(tile_bar(s_full, i), tile_phase(i));
+                // m of this segment: to be set here, or set by the other group.  S of this tile
+                // came after the other had handed over tile i - 2 at least, so what it may still
+                // read belongs to one of the last kMBufs - 1 segments.
                 if (!first) await(m_full + 8 * (seg & 1), (seg >> 1) & 1u);
-                else if (i > 0) await(before, before_phase);
                 __syncwarp();
                 tc_fence_after();
                 if (masked) {
                     // values behind the last key, and those that are not finite
                     const uint32_t slot = i % C::kSlots;
-                    await(v_full + 8 * slot, (i / C::kSlots) & 1u);
+                    await(tile_bar(v_full, i), tile_phase(i));
                     // 16-byte chunks in an order of the lane's own, so that neighbouring rows,
                     // 128 bytes apart, meet different banks
                     const uint32_t v = s0 + C::kRingV + slot * C::kTileBytes + at * 128;
@@ -873,13 +904,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        finite_or_zero(x2), finite_or_zero(x3));
                             }
                         }
-                        if (odd) *reinterpret_cast<volatile int *>(&ctl.odd[seg & 1]) = 1;
+                        if (odd) *reinterpret_cast<volatile int *>(&ctl.odd[seg % C::kMBufs]) = 1;
                     }
                     __syncwarp();
                 }
-                // The P buffer is free: its last product, two tiles ago, came before this S in the
-                // tensor core's order.
-                const uint32_t prow = s0 + C::kP + wg * C::kPBytes + at * 128;
+                // With three P buffers this one is free: its last product, three tiles ago, came
+                // before this S in the tensor core's order.  With two it is waited for.
+                const uint32_t prow = s0 + C::kP + i % C::kPBufs * C::kPBytes + at * 128;
+                if (C::kPBufs == 2 && i >= 2) await(tile_bar(o_done, i - 2), tile_phase(i - 2));
+                __syncwarp();
                 // 1: m has to be set, 2: to be raised.  m is the maximum over the first tile, or,
                 // where every row sees all of it, over one warp's 32 keys, which does as well and
                 // is one exchange for a warp.
@@ -911,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (task == 2 && !first) {
                         // O and l of the tiles before are scaled
                         const uint32_t ob = seg % C::kOBufs;
-                        await(o_done + 8 * ((i - 1) % C::kSlots), ((i - 1) / C::kSlots) & 1u);
+                        await(tile_bar(o_done, i - 1), tile_phase(i - 1));
                         __syncwarp();
                         tc_fence_after();
                         for (int c0 = 0; c0 < n; c0 += 16) {
@@ -964,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sts128(to + (((u + 1) ^ (at & 7)) << 4), word[4], word[5], word[6], word[7]);
                     }
                     // this tile's turn, and what has become of m
-                    if (!first) await(before, before_phase);
+                    if (i > 0) await(before, before_phase);
                     const bool stale = *reinterpret_cast<volatile int *>(&ctl.epoch) != epoch;
                     if (!group_any(wg, stale || top > kRaise)) break;
                     task = group_any(wg, stale) ? 0 : 2;
@@ -972,12 +1005,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 mbar_arrive(p_full + 8 * wg);
-                if (kt + 1 == cur.kt_end) output(cur, seg);
+                // a unit's output: at once, since the next unit's O waits for it, or, with a
+                // second O buffer, after the group's next tile, when the last product is done
+                if (owed) {
+                    output(late, late_seg, late_tile);
+                    owed = false;
+                }
+                if (kt + 1 == cur.kt_end) {
+                    late = cur;
+                    late_seg = seg;
+                    late_tile = i;
+                    if (C::kOBufs == 1) output(late, late_seg, late_tile);
+                    else owed = true;
+                }
             }
             i -= kt - cur.kt_end;                 // the next segment's first tile
             ++seg;
             more = w.next(p);
         }
+        if (owed) output(late, late_seg, late_tile);
         if (tid == 0) p.desc[blockIdx.x] = desc;
     }
     tc_fence_before();
