@@ -73,24 +73,51 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_store_kernel(c
     const int rows = min(per_cta, n - row0);
     if (rows <= 0) return;
     const int pairs = p.rot / 2;
-    for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
-        const int r = i / pairs, j = i - r * pairs;
-        // angle / pi in [-1, 1]: fraction of a turn, times two
-        const double turns = static_cast<double>(p.position[row0 + r]) *
-                             static_cast<double>(p.inv_freq[j]) * 0.15915494309189533577;
-        float s, c;
-        sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &c);
-        turn[r][j] = make_float2(c * p.rope_scale, s * p.rope_scale);
-    }
-    __syncthreads();
     const int r = warp / p.share, row = row0 + r;
-    if (r >= rows) return;
+    const bool live = r < rows;
 
     // the lane's channels: ca .. ca + 3 and cb .. cb + 3; pair i is (a_i, b_i) of its factors
     const int sub = lane % kLanes;
     const bool halves = !kInterleaved && 8 * sub < p.rot;
     const int ca = halves ? 4 * sub : 8 * sub, cb = halves ? pairs + 4 * sub : 8 * sub + 4;
     const bool turns = 8 * sub < p.rot;
+    const int heads = p.Hq + 2 * p.Hkv;
+    const int step = p.share * kHeads;            // heads from a warp's unit to its next
+    const uint16_t *from = p.qkv + row * p.stride + ca;
+    const int gap = cb - ca, first = (warp - r * p.share) * kHeads;
+
+    // the next units' channels are on their way while these are worked on, the first ones
+    // while the sines are
+    uint2 na[kInFlight], nb[kInFlight];
+    auto fetch = [&](int h0) {
+#pragma unroll
+        for (int f = 0; f < kInFlight; ++f) {
+            const int head = h0 + f * step + lane / kLanes;
+            na[f] = nb[f] = make_uint2(0, 0);
+            if (head < heads) {
+                const uint16_t *x = from + static_cast<size_t>(head) * D;
+                na[f] = __ldg(reinterpret_cast<const uint2 *>(x));
+                nb[f] = __ldg(reinterpret_cast<const uint2 *>(x + gap));
+            }
+        }
+    };
+    int slot = -1;
+    if (live) {
+        fetch(first);
+        slot = p.slot[row];
+    }
+    for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
+        const int t = i / pairs, j = i - t * pairs;
+        // angle / pi in [-1, 1]: fraction of a turn, times two
+        const double turned = static_cast<double>(p.position[row0 + t]) *
+                              static_cast<double>(p.inv_freq[j]) * 0.15915494309189533577;
+        float s, c;
+        sincospif(2.0f * static_cast<float>(turned - rint(turned)), &s, &c);
+        turn[t][j] = make_float2(c * p.rope_scale, s * p.rope_scale);
+    }
+    __syncthreads();
+    if (!live) return;
+
     Factors fq, fk;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -106,32 +133,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_store_kernel(c
         fq.ac[i] = qa * t.x, fq.bs[i] = qb * t.y, fq.as[i] = qa * t.y, fq.bc[i] = qb * t.x;
         fk.ac[i] = ka * t.x, fk.bs[i] = kb * t.y, fk.as[i] = ka * t.y, fk.bc[i] = kb * t.x;
     }
-    const int slot = p.slot[row];
     const int page = slot / p.ps;
     const bool stored = slot >= 0 && page < p.num_pages;
     if (!stored && lane == 0) record_error(DSPARK_INVALID_PAGE);
     const size_t place =
         stored ? (static_cast<size_t>(page) * p.Hkv * p.ps + (slot - page * p.ps)) * D : 0;
-    const int heads = p.Hq + 2 * p.Hkv;
-    const int step = p.share * kHeads;            // heads from a warp's unit to its next
-    const uint16_t *from = p.qkv + row * p.stride + ca;
-    const int gap = cb - ca, first = (warp - r * p.share) * kHeads;
-
-    // the next units' channels are on their way while these are worked on
-    uint2 na[kInFlight], nb[kInFlight];
-    auto fetch = [&](int h0) {
-#pragma unroll
-        for (int f = 0; f < kInFlight; ++f) {
-            const int head = h0 + f * step + lane / kLanes;
-            na[f] = nb[f] = make_uint2(0, 0);
-            if (head < heads) {
-                const uint16_t *x = from + static_cast<size_t>(head) * D;
-                na[f] = __ldg(reinterpret_cast<const uint2 *>(x));
-                nb[f] = __ldg(reinterpret_cast<const uint2 *>(x + gap));
-            }
-        }
-    };
-    fetch(first);
     for (int u0 = first; u0 < heads; u0 += kInFlight * step) {
         const int h0 = u0 + lane / kLanes;
         uint2 xa[kInFlight], xb[kInFlight];
