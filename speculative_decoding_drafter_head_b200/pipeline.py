@@ -28,11 +28,24 @@ t + 1, is no longer read by then, and every lengths slot is read by its own step
 verification before the next fork.  Both dependencies live inside one step, so a step
 can be captured as one CUDA graph (one graph per ring phase) and replayed.
 
+``VerifyPass`` keeps what the target's verification pass needs between the scheduler and the
+verification: the paged cache of every layer, its block tables and free pages, and the
+buffers of one step's ragged batch.  A step is
+
+    L = sched.lengths(t)                              # or step()'s L_out
+    vp.layout(L, anchor, x, accepted)                 # batch of this step, pages, slots
+    for layer in range(layers):                       # the target's own products around it
+        out = vp.attend(layer, qkv(layer), q_weight, k_weight)
+    verify_prefix(x, L, target, accepted, bonus)
+
+with every length on the device, so the whole step can be captured as one CUDA graph.
+
 This module only orders launches of the library's kernels; it computes nothing.
 """
 from __future__ import annotations
 
-from . import schedule_prefix, workspace_bytes
+from . import (qk_norm_rope_store, schedule_prefix, verify_attention,
+               verify_attention_workspace_bytes, verify_layout, workspace_bytes)
 
 
 def scores_slot(t: int, lag: int) -> int:
@@ -112,3 +125,53 @@ class LaggedScheduler:
         """(N*, objective) tensors of the schedule used at step t."""
         o = scores_slot(t, self.lag)
         return self.N[o], self.obj[o]
+
+
+class VerifyPass:
+    """Paged cache, block tables and batch buffers of the target's verification pass."""
+
+    def __init__(self, B: int, gamma: int, layers: int, Hq: int, Hkv: int, D: int, page_size: int,
+                 num_pages: int, max_pages: int, inv_freq=None, interleaved: bool = False,
+                 rope_scale: float = 1.0, eps: float = 1e-6, scale=None, device="cuda"):
+        import torch
+        i32 = dict(dtype=torch.int32, device=device)
+        bf16 = dict(dtype=torch.bfloat16, device=device)
+        rows = B * (gamma + 1)
+        self.gamma, self.page_size = gamma, page_size
+        self.rope = dict(eps=eps, inv_freq=inv_freq, interleaved=interleaved, rope_scale=rope_scale)
+        self.scale = scale
+        # the cache's state: all request slots idle, all pages free
+        self.context = torch.full((B,), -1, **i32)
+        self.rows = torch.zeros(B, **i32)
+        self.pages = torch.zeros(B, max_pages, **i32)
+        self.held = torch.zeros(B, **i32)
+        self.free_pages = torch.arange(num_pages, **i32)
+        self.free_count = torch.full((1,), num_pages, **i32)
+        cache = (layers, num_pages, Hkv, page_size, D)
+        self.k_cache, self.v_cache = torch.zeros(cache, **bf16), torch.zeros(cache, **bf16)
+        # one step's batch
+        self.row_start = torch.zeros(B + 1, **i32)
+        self.position, self.slot, self.token = (torch.zeros(rows, **i32) for _ in range(3))
+        self.q, self.out = (torch.zeros(rows, Hq, D, **bf16) for _ in range(2))
+        self.workspace = torch.empty(verify_attention_workspace_bytes(Hq, Hkv, D),
+                                     dtype=torch.uint8, device=device)
+
+    def layout(self, L, anchor, x, accepted=None, stream=None):
+        """Lay out this step's batch (see dspark_verify_layout): L [B] (cut in place where pages
+        run out), anchor [B], x [B, gamma], and, from the second step of a request on, the
+        accepted counts of the last step.  Fills row_start, position, slot and token."""
+        verify_layout(L, self.context, self.rows, self.pages, self.held, self.free_pages,
+                      self.free_count, self.row_start, self.position, self.slot, self.page_size,
+                      self.gamma, anchor=anchor, x=x, token=self.token, accepted=accepted,
+                      stream=stream)
+
+    def attend(self, layer: int, qkv, q_weight=None, k_weight=None, stream=None):
+        """One layer's attention of the batch: qkv [B (gamma + 1), (Hq + 2 Hkv) D] normalised,
+        rotated and stored, then attended.  Returns the buffer [B (gamma + 1), Hq, D], which the
+        next call writes again."""
+        k, v = self.k_cache[layer], self.v_cache[layer]
+        qk_norm_rope_store(qkv, self.position, self.slot, self.row_start[-1:], self.q, k, v,
+                           q_weight=q_weight, k_weight=k_weight, stream=stream, **self.rope)
+        verify_attention(self.q, k, v, self.pages, self.context, self.row_start, self.out,
+                         self.workspace, scale=self.scale, stream=stream)
+        return self.out

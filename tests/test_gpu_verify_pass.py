@@ -581,6 +581,74 @@ def test_pass_together_captured(ds):
     assert max(p for _, p in hist) > 20
 
 
+def test_verify_pass_steps(ds):
+    """pipeline.VerifyPass over two layers, with requests that come and go, against the plain
+    forms: every row attends to all of its request's tokens that stuck, and to its own step's."""
+    import torch
+    from speculative_decoding_drafter_head_b200.pipeline import VerifyPass
+    rng = np.random.default_rng(3)
+    B, gamma, layers, Hq, Hkv, D, ps = 5, 3, 2, 6, 2, 64, 16
+    inv = (1e4 ** (-torch.arange(16, dtype=torch.float64) / 16)).float().cuda()
+    vp = VerifyPass(B, gamma, layers, Hq, Hkv, D, ps, num_pages=24, max_pages=6, inv_freq=inv,
+                    interleaved=True, scale=0.2)
+    side = torch.cuda.Stream()
+    hist = [{} for _ in range(layers)]
+    accepted, ctx, rows = None, np.full(B, -1), np.zeros(B, int)
+    for t in range(10):
+        if t == 0:
+            vp.context.copy_(i32([0, 0, -1, 0, -1]))
+            ctx = np.array([0, 0, -1, 0, -1])
+        elif t == 4:                                           # request 1 ends, slot 4 starts
+            vp.context[1], vp.context[4] = -1, 0
+            ctx[1], ctx[4] = -1, 0
+            hist = [{k: v for k, v in h.items() if k[0] not in (1, 4)} for h in hist]
+            accepted[4] = -1
+        if accepted is not None:
+            ctx = np.where(ctx >= 0, ctx + np.minimum(accepted + 1, rows), ctx)
+        L = rng.integers(0, gamma + 1, B)
+        x, anchor = rng.integers(0, 99, (B, gamma)), rng.integers(0, 99, B)
+        acc_d = None if accepted is None else i32(accepted)
+        d = i32(L), i32(anchor), i32(x)
+        torch.cuda.synchronize()
+        vp.layout(*d, acc_d, stream=side)
+        rows = np.where(ctx >= 0, L + 1, 0)
+        req = np.repeat(np.arange(B), rows)
+        n = len(req)
+        pos = np.concatenate([np.arange(ctx[b], ctx[b] + rows[b]) for b in range(B)])
+        side.synchronize()
+        np.testing.assert_array_equal(host(vp.position)[:n], pos)
+        np.testing.assert_array_equal(host(vp.context), ctx)
+        assert int(vp.row_start[-1]) == n
+        for layer in range(layers):
+            qkv = torch.randn(B * (gamma + 1), (Hq + 2 * Hkv) * D, device="cuda").bfloat16()
+            torch.cuda.synchronize()
+            out = vp.attend(layer, qkv, stream=side)
+            side.synchronize()
+            assert ds.get_error() == 0
+            r64 = qkv[:n].double().cpu().numpy().reshape(n, Hq + 2 * Hkv, D)
+            q = vp.q.double().cpu().numpy()
+            want_q = ref.head(r64[:, :Hq], None, 0, pos, inv.cpu().numpy(), True, 1.0)
+            assert (np.abs(q[:n] - want_q) <= 2.0 ** -8 * np.abs(want_q) + 2.0 ** -16).all()
+            k64 = ref.head(r64[:, Hq:Hq + Hkv], None, 0, pos, inv.cpu().numpy(), True, 1.0)
+            k64 = torch.from_numpy(k64).bfloat16().double().numpy()    # one rounding, as stored
+            for r in range(n):
+                hist[layer][int(req[r]), int(pos[r])] = (k64[r], r64[r, Hq + Hkv:])
+            got = out.double().cpu().numpy()
+            for r in range(n):
+                keys = [hist[layer][int(req[r]), j] for j in range(int(pos[r]) + 1)]
+                for h in range(Hq):
+                    kk, vv = (np.stack([a[i][h // 3] for a in keys]) for i in range(2))
+                    sc = kk @ q[r, h] * 0.2
+                    p = np.exp(sc - sc.max())
+                    p /= p.sum()
+                    # as elsewhere, and a key that rounds the other way: 2^-8 of it, which moves
+                    # a score by up to 0.2 x 2^-8 |q| |k| < 2^-2 here, for a few keys of many
+                    tol = 2.0 ** -8 * np.abs(p @ vv) + 2.0 ** -5 * (p @ np.abs(vv)) + 1e-6
+                    assert (np.abs(got[r, h] - p @ vv) <= tol).all()
+        accepted = np.array([rng.integers(0, L[b] + 1) for b in range(B)])
+    assert int(vp.free_count) + int(vp.held.sum()) == 24       # no page lost
+
+
 def test_two_streams_at_once(ds):
     """Two calls at once with a workspace each, on streams of their own."""
     import torch
