@@ -162,7 +162,7 @@ __device__ __forceinline__ void load_request(const Params &p, int b, int &ctx, i
         min(static_cast<long long>(p.max_pages) * p.ps, static_cast<long long>(INT32_MAX)));
     bad = s0 != start || s1 != start + rows;
     ctx = max(c, 0);
-    if (rows > room || ctx > room - rows) {
+    if (rows > 0 && (rows > room || ctx > room - rows)) {
         bad = true;
         rows = min(rows, room);
         ctx = room - rows;

@@ -347,6 +347,7 @@ CASES = [
     ([127, 126, 120, 0], [2, 2, 17, 17], 8, 2, 128, 16),    # rows across a tile's end
     ([5, -1, 300, -1, 40], [3, 0, 1, 0, 2], 10, 5, 64, 32),  # idle slots
     ([-1, -1], [0, 0], 4, 4, 64, 16),                       # nothing at all
+    ([9000, 70, 1 << 30], [0, 3, 0], 4, 4, 64, 16),         # any context without rows
     ([1000, 3, 77], [17, 9, 1], 32, 8, 128, 16),            # 68 rows to a key head
     ([513], [25], 64, 8, 128, 64),                          # 200 rows to a key head
     ([63, 260], [7, 8], 112, 1, 128, 32),                   # every token a tile of rows
