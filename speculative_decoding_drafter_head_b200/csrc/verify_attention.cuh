@@ -52,7 +52,7 @@ using vplan::kTileKeys;
 
 constexpr int kMaxB = 4096;
 constexpr int kMaxCtas = 160;                     // grid: one CTA per SM, at most this many
-constexpr int kMaxRows = 112;                     // rows of a query tile
+constexpr int kMaxRows = vplan::kMostRows;        // rows of a query tile
 constexpr int kThreads = 384;
 constexpr int kSoftThreads = 128;               // of each of the two softmax groups
 constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpQ = 11;
@@ -213,7 +213,7 @@ struct Walk {
     int base, l_ctx, l_rows, l_start;             // request base + lane
     int b, ctx, rows, start;
     int h, qt, kt, kt_end, tiles;                 // segment [kt, kt_end) of the unit's tiles
-    long long left;
+    long long left, unit;                         // places left, and the first of the unit
 
     __device__ __forceinline__ void load(const Params &p)
     {
@@ -231,21 +231,28 @@ struct Walk {
     }
     __device__ __forceinline__ vplan::Request request(const Params &p) const
     {
-        return vplan::Request{ctx, rows, p.tokens};
+        return vplan::Request{ctx, rows, p.tokens, p.group};
     }
-    // From place `at` of the unit on; false when the CTA's share ends before a key tile.
+    // From place `at` of the unit on; false when the CTA's share ends before a key tile starts.
     __device__ __forceinline__ bool segment(const Params &p, int at)
     {
-        tiles = request(p).key_tiles(qt);
-        const int n = static_cast<int>(
-            min(static_cast<long long>(vplan::kUnitCost + tiles - at), left));
+        const vplan::Request r = request(p);
+        tiles = r.key_tiles(qt);
+        const int per = r.tile_places(qt), all = vplan::kUnitPlaces + tiles * per;
+        const int n = static_cast<int>(min(static_cast<long long>(all - at), left));
         left -= n;
-        kt = max(at - vplan::kUnitCost, 0);
-        kt_end = at + n - vplan::kUnitCost;
+        kt = vplan::tile_at(at, per);
+        kt_end = min(vplan::tile_at(at + n, per), tiles);
         return kt_end > kt;
     }
+    __device__ __forceinline__ long long last_place(const Params &p) const
+    {
+        return unit + vplan::kUnitPlaces + static_cast<long long>(tiles - 1) *
+                                               request(p).tile_places(qt);
+    }
     // The segment at place `off` of request b0; false when there is none.
-    __device__ __forceinline__ bool begin(const Params &p, int b0, long long off, long long count)
+    __device__ __forceinline__ bool begin(const Params &p, int b0, long long off, long long first,
+                                          long long count)
     {
         left = count;
         if (count <= 0) return false;
@@ -254,11 +261,13 @@ struct Walk {
         take(b0);
         int at;
         place(request(p), off, h, qt, at);
-        return segment(p, at);
+        unit = first - at;
+        return segment(p, at) || next(p);
     }
     __device__ __forceinline__ bool next(const Params &p)
     {
         if (left <= 0) return false;
+        unit += vplan::kUnitPlaces + static_cast<long long>(tiles) * request(p).tile_places(qt);
         if (++qt == request(p).query_tiles()) {
             qt = 0;
             if (++h == p.Hkv) {
@@ -409,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool bad;
         load_request(p, r, ctx, rows, start, bad);
         if (bad && blockIdx.x == 0) record_error(DSPARK_INVALID_TOKEN);
-        if (rows > 0) mine += vplan::Request{ctx, rows, p.tokens}.per_head() * p.Hkv;
+        if (rows > 0) mine += vplan::Request{ctx, rows, p.tokens, p.group}.per_head() * p.Hkv;
     }
     long long sum = mine;
 #pragma unroll
@@ -474,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool bad;
             load_request(p, r, ctx, rows, start, bad);
             const long long n =
-                rows > 0 ? vplan::Request{ctx, rows, p.tokens}.per_head() * p.Hkv : 0;
+                rows > 0 ? vplan::Request{ctx, rows, p.tokens, p.group}.per_head() * p.Hkv : 0;
             if (t0 < at + n) {
                 ctl.start_b = r;
                 ctl.start_off = t0 - at;
@@ -489,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
     Walk w = {};
-    bool more = w.begin(p, t1 > t0 ? ctl.start_b : 0, t1 > t0 ? ctl.start_off : 0, t1 - t0);
+    bool more = w.begin(p, t1 > t0 ? ctl.start_b : 0, t1 > t0 ? ctl.start_off : 0, t0, t1 - t0);
 
     if (warp == kWarpK || warp == kWarpV) {
         // ---------------------------------------------------- K or V pages into the ring
@@ -856,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             cur.ends = w.kt_end == w.tiles;
             if (cur.starts && !cur.ends)
                 desc = make_int4(cur.row0, cur.h, cur.rows,
-                                 vplan::cta_of(T, t1 - 1 + (w.tiles - w.kt_end), G) - cta + 1);
+                                 vplan::cta_of(T, w.last_place(p), G) - cta + 1);
             const int n = (cur.rows + 15) & ~15;
             float *m_row = m_s + seg % C::kMBufs * kN;
             int kt = cur.kt + ((i & 1) == static_cast<uint32_t>(wg) ? 0 : 1);

@@ -3,10 +3,13 @@
 // A unit is (request, key head, query tile): up to `tokens` of the request's rows, all the
 // query heads of one key head, against the keys that the tile's last row sees, in key tiles
 // of 128.  All units stand in one line (requests, then key heads, then query tiles), each as
-// kUnitCost places, what starting and ending it costs in key tiles, and then one place a key
-// tile; CTA c of G takes the places from floor(T c / G) to floor(T (c + 1) / G) of the T: equal
-// work whatever the lengths, a function of the lengths alone.  A unit whose tiles are cut by a
-// border is joined from its parts.
+// kUnitPlaces places, what starting and ending it costs, and then tile_places() a key tile, what
+// a tile costs; a tile belongs to where its first place is.  CTA c of G takes the places from
+// floor(T c / G) to floor(T (c + 1) / G) of the T: equal work whatever the lengths, a function
+// of the lengths alone.  A unit whose tiles are cut by a border is joined from its parts.
+//
+// A tile's cost is its 64 KB and, a little, its rows: tiles of 16 rows took 2430 cycles, of 48
+// 2680 and of 80 2860 where all of them shared the memory's rate.
 //
 // Plain integer arithmetic, the same on the host and the device.
 #pragma once
@@ -23,7 +26,10 @@ namespace dspark {
 namespace vplan {
 
 constexpr int kTileKeys = 128;
-constexpr int kUnitCost = 3;
+constexpr int kTilePlaces = 24;                   // of a tile, and one for each 16 rows
+constexpr int kUnitPlaces = 75;                   // of a unit: three tiles of 16 rows
+constexpr int kMostRows = 112;
+constexpr int kMostPlaces = kTilePlaces + kMostRows / 16;
 
 // a / b, both at least 0: a 64-bit division takes the device several times a 32-bit one's time,
 // and the kernel's first copies wait for these
@@ -60,7 +66,8 @@ DSPARK_HD_CALL long long floor_sum(long long n, long long a, long long b)
 
 struct Request {
     int ctx, rows;     // rows > 0
-    int tokens;        // rows of a query tile
+    int tokens;        // tokens of a query tile
+    int group;         // rows (query heads) of a token
 
     DSPARK_HD int query_tiles() const { return (rows + tokens - 1) / tokens; }
     // keys that query tile qt sees, and its key tiles
@@ -70,16 +77,23 @@ struct Request {
         return ctx + static_cast<int>(end < rows ? end : rows);
     }
     DSPARK_HD int key_tiles(int qt) const { return (keys(qt) - 1) / kTileKeys + 1; }
+    DSPARK_HD int unit_rows(int qt) const
+    {
+        const long long left = rows - static_cast<long long>(qt) * tokens;
+        return static_cast<int>(left < tokens ? left : tokens) * group;
+    }
+    DSPARK_HD int tile_places(int qt) const { return kTilePlaces + (unit_rows(qt) + 15) / 16; }
     // places of query tiles 0 .. qt - 1, all but the last of which may be full
     DSPARK_HD long long before(int qt) const
     {
         if (qt <= 0) return 0;
         const int full = qt < query_tiles() ? qt : query_tiles() - 1;
-        long long sum = full > 0 ? floor_sum(full, tokens, static_cast<long long>(ctx) + tokens +
-                                                               kTileKeys - 1)
-                                 : 0;
-        if (full < qt) sum += key_tiles(full);
-        return sum + static_cast<long long>(qt) * kUnitCost;
+        long long sum = 0;
+        if (full > 0)
+            sum = floor_sum(full, tokens, static_cast<long long>(ctx) + tokens + kTileKeys - 1) *
+                  tile_places(0);
+        if (full < qt) sum += static_cast<long long>(key_tiles(full)) * tile_places(full);
+        return sum + static_cast<long long>(qt) * kUnitPlaces;
     }
     DSPARK_HD long long per_head() const { return before(query_tiles()); }
 };
@@ -91,8 +105,20 @@ DSPARK_HD int cta_of(long long T, long long t, int G)
 {
     return static_cast<int>(quotient((t + 1) * G - 1, T));
 }
-// CTAs that take part: each has at least one place
-DSPARK_HD int ctas(long long T, int most) { return T < most ? static_cast<int>(T) : most; }
+// CTAs that take part: each has as many places as the largest tile at least, so that no CTA
+// between a unit's first and last is without a tile of it
+DSPARK_HD int ctas(long long T, int most)
+{
+    if (T / kMostPlaces >= most) return most;
+    return T < kMostPlaces ? (T > 0) : static_cast<int>(T / kMostPlaces);
+}
+// the first key tile that starts at place `at` of a unit or later
+DSPARK_HD int tile_at(long long at, int tile_places)
+{
+    return at <= kUnitPlaces
+               ? 0
+               : static_cast<int>(quotient(at - kUnitPlaces + tile_places - 1, tile_places));
+}
 
 // Place `at` of a request with per_head() * heads places: key head, query tile, place in the unit.
 DSPARK_HD void place(const Request &r, long long at, int &h, int &qt, int &in_unit)

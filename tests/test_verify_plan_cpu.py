@@ -20,14 +20,20 @@ int main()
     std::mt19937 rng(7);
     auto in = [&](int lo, int hi) { return lo + static_cast<int>(rng() % (hi - lo + 1)); };
     for (int it = 0; it < 3000; ++it) {                    // closed forms, far contexts
-        Request r{in(0, it % 2 ? 3000 : 2000000000), in(1, it % 3 ? 25 : 900), in(1, 112)};
+        const int group = in(1, 20);
+        Request r{in(0, it % 2 ? 3000 : 2000000000), in(1, it % 3 ? 25 : 900), in(1, 112 / group),
+                  group};
         long long sum = 0;
         for (int q = 0; q < r.query_tiles(); ++q) {
             CHECK(r.before(q) == sum);
-            const long long keys = r.ctx + std::min<long long>(r.rows, (q + 1LL) * r.tokens);
-            CHECK(r.keys(q) == keys);
-            CHECK(r.key_tiles(q) == (keys + kTileKeys - 1) / kTileKeys);
-            sum += kUnitCost + r.key_tiles(q);
+            const long long end = std::min<long long>(r.rows, (q + 1LL) * r.tokens);
+            CHECK(r.keys(q) == r.ctx + end);
+            CHECK(r.key_tiles(q) == (r.ctx + end + kTileKeys - 1) / kTileKeys);
+            const int rows = static_cast<int>(end - static_cast<long long>(q) * r.tokens) * group;
+            CHECK(r.unit_rows(q) == rows && rows >= 1 && rows <= kMostRows);
+            CHECK(r.tile_places(q) == kTilePlaces + (rows + 15) / 16);
+            CHECK(r.tile_places(q) <= kMostPlaces);
+            sum += kUnitPlaces + static_cast<long long>(r.key_tiles(q)) * r.tile_places(q);
         }
         CHECK(r.per_head() == sum);
         const int heads = in(1, 8);
@@ -35,25 +41,34 @@ int main()
         int h, qt, in_unit;
         place(r, at, h, qt, in_unit);
         CHECK(h * sum + r.before(qt) + in_unit == at);
-        CHECK(in_unit >= 0 && in_unit < kUnitCost + r.key_tiles(qt));
+        const int per = r.tile_places(qt), tiles = r.key_tiles(qt);
+        CHECK(in_unit >= 0 && in_unit < kUnitPlaces + static_cast<long long>(tiles) * per);
+        const int t = tile_at(in_unit, per);
+        CHECK(t <= tiles && (t == 0 || kUnitPlaces + (t - 1LL) * per < in_unit));
+        CHECK(t == tiles || kUnitPlaces + static_cast<long long>(t) * per >= in_unit);
     }
     for (int it = 0; it < 400; ++it) {                     // whole batches
-        const int B = in(1, 40), heads = in(1, 4), tokens = in(1, 30), most = 148;
+        const int B = in(1, 40), heads = in(1, 4), most = 148, group = in(1, 8);
+        const int tokens = in(1, 112 / group);
         std::vector<Request> req;
         long long T = 0;
         for (int b = 0; b < B; ++b) {
-            req.push_back(Request{in(0, it % 4 ? 900 : 30000), in(1, 25), tokens});
+            req.push_back(Request{in(0, it % 4 ? 900 : 30000), in(1, 25), tokens, group});
             T += req.back().per_head() * heads;
         }
         const int G = ctas(T, most);
-        // the line, place by place: (unit, tile) or overhead
+        CHECK(G >= 1 && G <= most && (G == 1 || T / G >= kMostPlaces));
+        // the line, place by place: the unit, and the tile that starts there or -1
         std::vector<int> unit_of, tile_of, tiles;
         for (auto &r : req)
             for (int h = 0; h < heads; ++h)
                 for (int q = 0; q < r.query_tiles(); ++q) {
-                    for (int c = 0; c < kUnitCost + r.key_tiles(q); ++c) {
+                    const int per = r.tile_places(q);
+                    for (int c = 0; c < kUnitPlaces + r.key_tiles(q) * per; ++c) {
+                        const int in_tiles = c - kUnitPlaces;
                         unit_of.push_back(static_cast<int>(tiles.size()));
-                        tile_of.push_back(c - kUnitCost);
+                        tile_of.push_back(in_tiles >= 0 && in_tiles % per == 0 ? in_tiles / per
+                                                                               : -1);
                     }
                     tiles.push_back(r.key_tiles(q));
                 }
