@@ -134,9 +134,10 @@ struct Ctl {
     unsigned long long k_full[kTileBars], v_full[kTileBars], s_full[kTileBars], o_done[kTileBars];
     unsigned long long p_full[2], m_full[2];
     unsigned long long q_full[2], q_empty[2], o_empty[2], drain;
-    long long start_off;                          // first place in its request
+    struct {
+        int b, ctx, rows, start, h, qt, at;       // the CTA's first place
+    } first;
     unsigned long long sums[kThreads / 32];
-    int start_b;
     uint32_t tmem;
     int abort;
     int epoch;                                    // times that a reference m rose
@@ -250,19 +251,17 @@ struct Walk {
         return unit + vplan::kUnitPlaces + static_cast<long long>(tiles - 1) *
                                                request(p).tile_places(qt);
     }
-    // The segment at place `off` of request b0; false when there is none.
-    __device__ __forceinline__ bool begin(const Params &p, int b0, long long off, long long first,
+    // The first segment of the `count` places from `first` on; false when there is none.
+    __device__ __forceinline__ bool begin(const Params &p, const Ctl &ctl, long long first,
                                           long long count)
     {
         left = count;
         if (count <= 0) return false;
-        base = b0;
-        load(p);
-        take(b0);
-        int at;
-        place(request(p), off, h, qt, at);
-        unit = first - at;
-        return segment(p, at) || next(p);
+        b = ctl.first.b, ctx = ctl.first.ctx, rows = ctl.first.rows, start = ctl.first.start;
+        h = ctl.first.h, qt = ctl.first.qt;
+        base = -1;                                // nothing loaded yet
+        unit = first - ctl.first.at;
+        return segment(p, ctl.first.at) || next(p);
     }
     __device__ __forceinline__ bool next(const Params &p)
     {
@@ -272,6 +271,10 @@ struct Walk {
             qt = 0;
             if (++h == p.Hkv) {
                 h = 0;
+                if (base < 0) {
+                    base = b;
+                    load(p);
+                }
                 unsigned more = __ballot_sync(
                     0xFFFFFFFFu, l_rows > 0 && base + static_cast<int>(threadIdx.x & 31) > b);
                 while (!more) {
@@ -461,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     long long T = 0, before = 0;
-#pragma unroll 1
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += ctl.sums[w];
         T += ctl.sums[w];
@@ -472,21 +475,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long t0 = cta < G ? vplan::first_place(T, cta, G) : 0;
     const long long t1 = cta < G ? vplan::first_place(T, cta + 1, G) : 0;
     if (t1 > t0 && before <= t0 && t0 < before + mine) {
+        // one thread finds the CTA's first place, and has its page ids fetched meanwhile
         long long at = before;
         for (int r = r0; r < min(r0 + per, p.B); ++r) {
-            if (r + 1 == min(r0 + per, p.B)) {    // the last one it can be
-                ctl.start_b = r;
-                ctl.start_off = t0 - at;
-                break;
-            }
             int ctx, rows, start;
             bool bad;
             load_request(p, r, ctx, rows, start, bad);
-            const long long n =
-                rows > 0 ? vplan::Request{ctx, rows, p.tokens, p.group}.per_head() * p.Hkv : 0;
+            if (rows == 0) continue;
+            const vplan::Request q{ctx, rows, p.tokens, p.group};
+            const long long n = q.per_head() * p.Hkv;
             if (t0 < at + n) {
-                ctl.start_b = r;
-                ctl.start_off = t0 - at;
+                int h, qt, in_unit;
+                place(q, t0 - at, h, qt, in_unit);
+                prefetch_l2(p.pages + static_cast<size_t>(r) * p.max_pages +
+                            min(vplan::tile_at(in_unit, q.tile_places(qt)), q.key_tiles(qt) - 1) *
+                                (kTileKeys / p.ps));
+                ctl.first.b = r, ctl.first.ctx = ctx, ctl.first.rows = rows;
+                ctl.first.start = start, ctl.first.h = h, ctl.first.qt = qt;
+                ctl.first.at = in_unit;
                 break;
             }
             at += n;
@@ -498,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
     Walk w = {};
-    bool more = w.begin(p, t1 > t0 ? ctl.start_b : 0, t1 > t0 ? ctl.start_off : 0, t0, t1 - t0);
+    bool more = w.begin(p, ctl, t0, t1 - t0);
 
     if (warp == kWarpK || warp == kWarpV) {
         // ---------------------------------------------------- K or V pages into the ring
