@@ -363,8 +363,8 @@ int dspark_verify_layout(int32_t *L, const int32_t *anchor, const int32_t *x,
  *   qkv [row_capacity, qkv_stride] bf16, qkv_stride >= (Hq + 2 Hkv) D
  *   n_rows [1] int32 (row_start + B of dspark_verify_layout)
  *   q_out [row_capacity, Hq, D] bf16; rows from n_rows on are left as they are
- *   k_cache, v_cache [num_pages, Hkv, page_size, D] bf16, written at slot[r]; none may
- *   overlap qkv.  A slot outside [0, num_pages page_size) records DSPARK_INVALID_PAGE and
+ *   k_cache, v_cache [num_pages, Hkv, page_size, D] bf16, written at slot[r].  No output
+ *   may overlap qkv.  A slot outside [0, num_pages page_size) records DSPARK_INVALID_PAGE and
  *   its key and value are not stored.  Slots of a call must differ from one another.
  * Supported: D 64 or 128; rot_dim a multiple of 16 in [0, D]; qkv_stride % 8 == 0;
  * Hq, Hkv <= 1024; num_pages page_size < 2^31; bf16 arrays 16-byte aligned.
@@ -385,7 +385,8 @@ int dspark_qk_norm_rope_store(const void *qkv, int64_t qkv_stride, const void *q
  *   out[r, h] = sum_j p_j v[j, h / g],  p = softmax_j(scale q[r, h] . k[j, h / g])
  * fp32 scores, sums and accumulators.  Keys that a row does not see take no part, whatever
  * their slots hold, NaN and infinities included.
- *   q, out [row_capacity, Hq, D] bf16; rows behind the last request's are left as they are
+ *   q, out [row_capacity, Hq, D] bf16, not overlapping; rows of out behind the last request's
+ *   are left as they are
  *   pages [B, max_pages], context [B], row_start [B + 1] int32 as dspark_verify_layout leaves
  *   them (context: -1 or any other value where a request has no rows)
  *   workspace, workspace_bytes >= dspark_verify_attention_workspace_bytes(Hq, Hkv, D);

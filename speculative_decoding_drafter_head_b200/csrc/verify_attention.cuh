@@ -19,7 +19,8 @@
 // tile, and stays until some score exceeds it by more than 2^24 in weight; then m rises to the
 // new maximum and O and l are scaled (one vote a tile, folded into the barrier that a tile
 // needs anyway).  bf16 weights keep their 8 bits at any magnitude, and O and l are fp32, so
-// a stale m costs no accuracy.  Rounding the weights to bf16 (2^-9 of each, twice under the
+// a stale m costs no accuracy.  A row without a finite score so far has an m below any, so that
+// its first one raises it.  Rounding the weights to bf16 (2^-9 of each, twice under the
 // output's own rounding) is what the tensor core's second product asks for.
 //
 // Masks: key j is seen by the rows from (j - context) g on, so a thread compares the row's
@@ -60,6 +61,7 @@ constexpr int kQThreads = 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWaitHintNs = 20000;
 constexpr float kRaise = 24.0f;                   // log2 of the weight at which m rises
+constexpr float kUnset = -1e30f;                  // m of a row that has met no finite score yet
 constexpr int kOnesBytes = 1152;                  // 8 x 2 core matrices of 128 B, one apart
 constexpr int kJoinThreads = 256;
 constexpr int kJoinSplit = 4;                     // CTAs that share a unit's rows
@@ -940,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (at < n) {
                             const float m = share ? red[((at >> 4) & 3) * kN + at] : max_of(at);
                             if (task == 1) {
-                                m_row[at] = m == -INFINITY ? 0.0f : m;
+                                m_row[at] = m == -INFINITY ? kUnset : m;
                             } else {
                                 const float old = m_row[at], now = fmaxf(old, m);
                                 m_row[at] = now;

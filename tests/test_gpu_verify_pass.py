@@ -418,6 +418,28 @@ def test_attention_rising_scores(ds):
     assert bool(((s["out"].double() - out).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_scores_minus_infinity(ds, D):
+    """Keys whose scores are -inf weigh nothing, however low the others are, in whole tiles too."""
+    import torch
+    s, start = make_attention([400, 60], [3, 2], 4, 2, D, 16, 12, spread=False)
+    n = s["k_cache"].shape[0] * 16
+    k = s["k_cache"].permute(0, 2, 1, 3).reshape(n, 2, D).nan_to_num(0.0)
+    k[:, :, 0] = -300.0 - 4.0 * (torch.arange(n, device="cuda") % 8)[:, None]
+    k[:300, 0, 0] = float("-inf")                           # request 0: two whole tiles and more
+    k[410:450, :, 0] = float("-inf")                        # request 1
+    s["k_cache"] = k.reshape(-1, 16, 2, D).permute(0, 2, 1, 3).contiguous()
+    s["q"].zero_()
+    s["q"][:, :, 0] = 1.0
+    with_workspace(ds, s)
+    ds.verify_attention(**s, scale=1.0)
+    assert ds.get_error() == 0
+    out, mag = reference_attention(s, 1.0)
+    assert bool(out[:int(start[-1])].isfinite().all())
+    tol = 2.0 ** -8 * out.abs() + (2.0 ** -7 + 2.0 ** -9) * mag
+    assert bool(((s["out"].double() - out).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
 def test_attention_hidden_values(ds, value):
     """A later row's key or value that is not finite reaches the rows that see it, no other."""
@@ -648,6 +670,35 @@ def test_verify_pass_steps(ds):
                     assert (np.abs(got[r, h] - p @ vv) <= tol).all()
         accepted = np.array([rng.integers(0, L[b] + 1) for b in range(B)])
     assert int(vp.free_count) + int(vp.held.sum()) == 24       # no page lost
+
+
+def test_graphs_that_share_a_workspace(ds):
+    """Two captured calls with one workspace, replayed in turn and with other lengths between."""
+    import torch
+    calls, graphs = [], []
+    for i in range(2):
+        s, start = make_attention([5000, 700 + i], [3, 17], 16, 2, 128, 32, 90 + i)
+        calls.append((with_workspace(ds, s), int(start[-1])))
+    calls[1][0]["workspace"] = calls[0][0]["workspace"]
+    for s, _ in calls:
+        ds.verify_attention(**s)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ds.verify_attention(**s)
+        graphs.append(g)
+    short = i32([100, 9])
+    for ctx in (None, short):
+        for s, _ in calls:
+            if ctx is not None:
+                s["context"].copy_(ctx)
+            s["out"].fill_(9.0)
+        for g in graphs * 2:
+            g.replay()
+        torch.cuda.synchronize()
+        assert ds.get_error() == 0
+        for s, total in calls:
+            check_attention(s, total, 128 ** -0.5)
 
 
 def test_two_streams_at_once(ds):
