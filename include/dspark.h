@@ -408,12 +408,13 @@ int dspark_verify_attention(const void *q, const void *k_cache, const void *v_ca
  * current device into *status (DSPARK_OK when nothing was recorded). */
 int dspark_get_error(dspark_stream_t stream, int *status);
 
-/* Limit in nanoseconds for every device-side wait of dspark_draft_step
- * (default 2e9).  Applies to launches made after the call. */
+/* Limit in nanoseconds for every device-side wait of dspark_draft_step and
+ * dspark_verify_attention (default 2e9).  Applies to launches made after the call. */
 int dspark_set_wait_timeout_ns(uint64_t ns);
 
 /* Test hook: the draft kernel's grid barrier waits for `extra` more arrivals than
- * there are CTAs, so that its bounded wait runs out (0 restores normal use). */
+ * there are CTAs, and the verification attention's tiles for as many more than there are
+ * threads, so that their bounded waits run out (0 restores normal use). */
 int dspark_debug_barrier_extra(int extra);
 
 #ifdef __cplusplus

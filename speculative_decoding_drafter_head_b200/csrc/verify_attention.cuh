@@ -77,6 +77,7 @@ struct Params {
     float2 *part_ml;                              // [ctas][2][kMaxRows] (m, l)
     float *part_o;                                // [ctas][2][kMaxRows][D]
     unsigned long long timeout_ns;
+    int barrier_extra;                            // test hook: arrivals that never come
 };
 
 // Workspace: descriptors, then (m, l), then O, two parts a CTA.
@@ -199,12 +200,14 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, Ctl &ct
     return __all_sync(0xFFFFFFFFu, wait(bar, parity, ctl, p));
 }
 
-// Bounded wait for this CTA's own copies and MMAs before it ends, whatever the abort flag.
-__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity, const Params &p)
+// Bounded wait for this CTA's own copies and MMAs before it ends, whatever the abort flag and
+// for a second at least.
+__device__ __noinline__ void wait_drain(uint32_t bar, uint32_t parity, const Params &p)
 {
     const uint64_t t0 = globaltimer_ns();
+    const unsigned long long limit = max(p.timeout_ns, 1000000000ull);
     while (!mbar_try_wait_sleep(bar, parity, kWaitHintNs))
-        if (globaltimer_ns() - t0 > p.timeout_ns) {
+        if (globaltimer_ns() - t0 > limit) {
             record_error(DSPARK_TIMEOUT);
             return;
         }
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(o_done + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(p_full + 8 * i, kSoftThreads);
+            mbar_init(p_full + 8 * i, kSoftThreads + p.barrier_extra);
             mbar_init(m_full + 8 * i, kSoftThreads);
             mbar_init(q_full + 8 * i, kQThreads);
             mbar_init(q_empty + 8 * i, 1);
@@ -1015,6 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // this tile's turn, and what has become of m
                     if (i > 0) await(before, before_phase);
+                    __syncwarp();
                     const bool stale = *reinterpret_cast<volatile int *>(&ctl.epoch) != epoch;
                     if (!group_any(wg, stale || top > kRaise)) break;
                     task = group_any(wg, stale) ? 0 : 2;

@@ -717,3 +717,28 @@ def test_two_streams_at_once(ds):
     assert ds.get_error() == 0
     for s, total in calls:
         check_attention(s, total, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("Hq, rows", [(8, 3), (32, 17)])      # both query tile sizes
+def test_attention_reports_timeout(ds, Hq, rows):
+    """An arrival that never comes: every wait runs out or sees the abort, the call reports it,
+    and the next one is right."""
+    import torch
+    s, start = make_attention([3000, 40, 700], [rows, 1, rows], Hq, 2, 128, 16, 21)
+    with_workspace(ds, s)
+    ds.verify_attention(**s)
+    assert ds.get_error() == 0
+    clean = s["out"].clone()
+    ds.set_wait_timeout_ns(200_000_000)
+    ds.debug_barrier_extra(1)
+    try:
+        ds.verify_attention(**s)
+        assert ds.get_error() == 6
+    finally:
+        ds.debug_barrier_extra(0)
+        ds.set_wait_timeout_ns(2_000_000_000)
+    s["out"].fill_(9.0)
+    ds.verify_attention(**s)
+    assert ds.get_error() == 0
+    assert bool((s["out"] == clean).all())
+    check_attention(s, int(start[-1]), 128 ** -0.5)
