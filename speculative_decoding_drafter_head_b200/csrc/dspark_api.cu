@@ -138,6 +138,32 @@ size_t sched_ws(int n)
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? DSPARK_OK : DSPARK_CUDA_ERROR; }
 
+// Launches a kernel of the verification pass.  These kernels wait for the stream's earlier
+// kernels themselves, before they touch memory (wait_for_prior_kernels), so that their launch
+// and set-up overlap the end of the one before: a step makes them by the hundred, each a few
+// microseconds long.
+template <class... Params, class... Args>
+int launch_overlapped(void (*kern)(Params...), dim3 grid, int threads, size_t smem, int cluster,
+                      dspark_stream_t stream, const Args &...args)
+{
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return from_cuda(cudaLaunchKernelEx(&cfg, kern, args...));
+}
+
 // STS-fit workspace: frozen products [2][N] f64, then label counts [gamma][n_t][n_bins]
 // u32, then fixed-point sums [gamma][n_t][n_bins] u64.
 struct StsFitLayout {
@@ -711,20 +737,7 @@ int dspark_verify_layout(int32_t *L, const int32_t *anchor, const int32_t *x,
     const long long most = static_cast<long long>(B) * (gamma + 1);
     int ctas = 1;
     while (ctas < 8 && most > static_cast<long long>(ctas) * threads) ctas *= 2;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return from_cuda(cudaLaunchKernelEx(&cfg, kern, prm));
+    return launch_overlapped(kern, dim3(ctas), threads, smem, ctas, stream, prm);
 }
 
 int dspark_qk_norm_rope_store(const void *qkv, int64_t qkv_stride, const void *q_weight,
@@ -783,8 +796,7 @@ int dspark_qk_norm_rope_store(const void *qkv, int64_t qkv_stride, const void *q
                                : Q::qk_norm_rope_store_kernel<64, false>)
                 : (interleaved ? Q::qk_norm_rope_store_kernel<128, true>
                                : Q::qk_norm_rope_store_kernel<128, false>);
-    kern<<<grid, Q::kThreads, 0, stream>>>(prm);
-    return from_cuda(cudaGetLastError());
+    return launch_overlapped(kern, dim3(grid), Q::kThreads, 0, 1, stream, prm);
 }
 
 size_t dspark_verify_attention_workspace_bytes(int Hq, int Hkv, int D)
@@ -887,20 +899,10 @@ int dspark_verify_attention(const void *q, const void *k_cache, const void *v_ca
         }
     }
     const int grid = dev->sms < A::kMaxCtas ? dev->sms : A::kMaxCtas;
-    kern<<<grid, A::kThreads, smem, stream>>>(tm_k, tm_v, prm);
-    if (cudaGetLastError() != cudaSuccess) return DSPARK_CUDA_ERROR;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(grid, A::kJoinSplit);
-    cfg.blockDim = dim3(A::kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return from_cuda(cudaLaunchKernelEx(
-        &cfg, D == 64 ? A::verify_join_kernel<64> : A::verify_join_kernel<128>, prm));
+    if (int st = launch_overlapped(kern, dim3(grid), A::kThreads, smem, 1, stream, tm_k, tm_v, prm))
+        return st;
+    return launch_overlapped(D == 64 ? A::verify_join_kernel<64> : A::verify_join_kernel<128>,
+                             dim3(grid, A::kJoinSplit), A::kJoinThreads, 0, 1, stream, prm);
 }
 
 size_t dspark_sts_fit_workspace_bytes(int N, int gamma, int n_t, int n_bins)

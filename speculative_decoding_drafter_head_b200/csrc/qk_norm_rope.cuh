@@ -24,6 +24,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace dspark {
 namespace qknorm {
@@ -67,6 +68,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_store_kernel(c
     __shared__ float2 turn[kWarps][kMaxPairs];    // (cos, sin) of the CTA's rows
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    launch_dependents();
+    wait_for_prior_kernels();
     const int n = min(max(*p.n_rows, 0), p.row_capacity);
     const int per_cta = kWarps / p.share;
     const int row0 = blockIdx.x * per_cta;

@@ -413,28 +413,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     launch_dependents();
     if (s0 % 1024 != 0) {                         // the swizzled tiles need it
+        wait_for_prior_kernels();
         if (tid == 0) record_error(DSPARK_BAD_LAUNCH);
         if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
         return;
     }
 
-    // ------------------------------------------------ this CTA's share of the tiles
-    long long mine = 0;
-    const int per = (p.B + kThreads - 1) / kThreads, r0 = tid * per;
-    for (int r = r0; r < min(r0 + per, p.B); ++r) {
-        int ctx, rows, start;
-        bool bad;
-        load_request(p, r, ctx, rows, start, bad);
-        if (bad && blockIdx.x == 0) record_error(DSPARK_INVALID_TOKEN);
-        if (rows > 0) mine += vplan::Request{ctx, rows, p.tokens, p.group}.per_head() * p.Hkv;
-    }
-    long long sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-        if (lane >= o) sum += u;
-    }
-    if (lane == 31) ctl.sums[warp] = sum;
     for (int i = tid; i < kOnesBytes / 4; i += kThreads)
         reinterpret_cast<uint32_t *>(smem + C::kOnes)[i] = 0x3F803F80u;
     const uint32_t k_full = smem_u32(ctl.k_full), v_full = smem_u32(ctl.v_full);
@@ -467,6 +451,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
         tmem_relinquish();
     }
+    wait_for_prior_kernels();
+
+    // ------------------------------------------------ this CTA's share of the tiles
+    long long mine = 0;
+    const int per = (p.B + kThreads - 1) / kThreads, r0 = tid * per;
+    for (int r = r0; r < min(r0 + per, p.B); ++r) {
+        int ctx, rows, start;
+        bool bad;
+        load_request(p, r, ctx, rows, start, bad);
+        if (bad && blockIdx.x == 0) record_error(DSPARK_INVALID_TOKEN);
+        if (rows > 0) mine += vplan::Request{ctx, rows, p.tokens, p.group}.per_head() * p.Hkv;
+    }
+    long long sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += u;
+    }
+    if (lane == 31) ctl.sums[warp] = sum;
     __syncthreads();
     long long T = 0, before = 0;
 #pragma unroll
@@ -1062,6 +1065,7 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads) verify_join_kernel(const Params p)
 {
     constexpr int kPer = D / 32;
+    launch_dependents();
     wait_for_prior_kernels();
     const int4 unit = p.desc[blockIdx.x];
     const int row0 = unit.x, h = unit.y, rows = unit.z, parts = unit.w;

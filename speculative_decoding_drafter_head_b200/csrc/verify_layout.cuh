@@ -89,6 +89,8 @@ __global__ void __launch_bounds__(kThreads) verify_layout_kernel(const Params p)
     int32_t *s_back = words + 3 * p.B, *s_ask = words + 4 * p.B, *s_row = words + 5 * p.B;
     const int tid = threadIdx.x;
     const int cta = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
+    launch_dependents();
+    wait_for_prior_kernels();
     const int room = static_cast<int>(
         min(static_cast<long long>(p.max_pages) * p.ps, static_cast<long long>(INT32_MAX)));
 
