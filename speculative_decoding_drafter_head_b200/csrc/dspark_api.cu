@@ -869,6 +869,8 @@ int dspark_verify_attention(const void *q, const void *k_cache, const void *v_ca
     prm.part_o = reinterpret_cast<float *>(ws + lay.o);
     prm.timeout_ns = g_timeout_ns.load();
     prm.barrier_extra = g_barrier_extra.load();
+    prm.ps_log2 = 4;
+    while ((1 << prm.ps_log2) < page_size) ++prm.ps_log2;
     // query tiles of 64 rows where a request's share of the row capacity (its gamma + 1 tokens,
     // when the batch layout made it) fits one, else of 112
     const bool wide = static_cast<long long>((row_capacity - 1) / B + 1) * prm.group > 64;

@@ -19,7 +19,9 @@
 //     y_a = inv (w_a c x_a - w_b s x_b),  y_b = inv (w_a s x_a + w_b c x_b)
 // (13000 rows of 48 heads of 128: 104 us with 16-byte chunks, shuffled partners and factors
 // from shared memory).  One warp takes a row, four units of two (D = 128) heads in flight; with
-// few rows the 8 warps of a CTA share one.
+// few rows the 8 warps of a CTA share one.  Measured (B200, device time): the 13000 rows 62 us,
+// 5.2 TB/s of the 6.47 a copy reaches; 550 rows of the same heads 5.5 us, one row 3.7 us, which
+// are a launch and two dependent loads.
 #pragma once
 #include <cuda_bf16.h>
 

@@ -20,8 +20,8 @@
 // new maximum and O and l are scaled (one vote a tile, folded into the barrier that a tile
 // needs anyway).  bf16 weights keep their 8 bits at any magnitude, and O and l are fp32, so
 // a stale m costs no accuracy.  A row without a finite score so far has an m below any, so that
-// its first one raises it.  Rounding the weights to bf16 (2^-9 of each, twice under the
-// output's own rounding) is what the tensor core's second product asks for.
+// its first one raises it.  The weights are rounded to bf16 (by 2^-8 of each at most, as the
+// output itself), which is what the tensor core's second product asks for.
 //
 // Masks: key j is seen by the rows from (j - context) g on, so a thread compares the row's
 // number with one number of its own.  Values behind the last key are cleared in shared memory
@@ -36,8 +36,14 @@
 // Warps: 0-3 and 4-7 softmax and output (thread = key of the tile, then channel of the output),
 // the groups taking tiles in turn, 8 and 9 copy K and V pages into rings of 32 KB tiles by TMA
 // (one box a page and 64 channels; one warp for both took 90 cycles a box, 3000 of a tile's
-// 2800 with pages of 16), 10 issues the MMAs, 11 copies Q.  S and P are double-buffered, so S of
-// the next tile and O of the last run beside the softmax.
+// 2800 with pages of 16), 10 issues the MMAs, 11 copies Q.  S is double-buffered and P at least
+// (three buffers where rows are 64), so S of the next tiles and O of the last run beside the
+// softmax.
+//
+// Measured (B200, device time): 64 requests, 32/8 heads of 128, 500-8000 keys, up to 17 rows
+// each 180 us, 6.1 TB/s of the 6.47 a copy reaches; 256 requests of one row, 32/4 heads 306 us,
+// 6.7 TB/s; one request of 131 thousand keys 92 us, 5.8 TB/s; one token over 700 keys 10 us, of which
+// 5 go before the first tile has come (launch, lengths, this CTA's share, page ids, the tile).
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -70,7 +76,7 @@ constexpr int kJoinAhead = 8;                     // parts whose O a row has in 
 struct Params {
     const uint16_t *q, *k_cache, *v_cache;
     const int32_t *pages, *context, *row_start;
-    int B, row_capacity, Hq, Hkv, group, tokens, ps, max_pages, num_pages;
+    int B, row_capacity, Hq, Hkv, group, tokens, ps, ps_log2, max_pages, num_pages;
     float scale_log2;                             // scale log2(e)
     uint16_t *out;
     int4 *desc;                                   // [ctas] the unit that starts a join
@@ -451,13 +457,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
         tmem_relinquish();
     }
+    // what the CTAs need first, into L2 while the kernel before ends: lengths, and page ids (of a
+    // table of up to a line a thread)
+    {
+        const int at = static_cast<int>(blockIdx.x) * kThreads + tid;
+        if (at <= (p.B * p.max_pages - 1) / 32) prefetch_l2(p.pages + 32 * at);
+        if (at <= (p.B - 1) / 32) {
+            prefetch_l2(p.context + 32 * at);
+            prefetch_l2(p.row_start + 32 * at);
+        }
+    }
     wait_for_prior_kernels();
 
     // ------------------------------------------------ this CTA's share of the tiles
     long long mine = 0;
     const int per = (p.B + kThreads - 1) / kThreads, r0 = tid * per;
+    int ctx = 0, rows = 0, start = 0;             // of this thread's last request
     for (int r = r0; r < min(r0 + per, p.B); ++r) {
-        int ctx, rows, start;
         bool bad;
         load_request(p, r, ctx, rows, start, bad);
         if (bad && blockIdx.x == 0) record_error(DSPARK_INVALID_TOKEN);
@@ -478,26 +494,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         T += ctl.sums[w];
     }
     before += sum - mine;
-    const int G = vplan::ctas(T, gridDim.x);
+    const vplan::Split split(T, gridDim.x);
     const int cta = blockIdx.x;
-    const long long t0 = cta < G ? vplan::first_place(T, cta, G) : 0;
-    const long long t1 = cta < G ? vplan::first_place(T, cta + 1, G) : 0;
+    const long long t0 = cta < split.G ? split.first(cta) : 0;
+    const long long t1 = cta < split.G ? split.first(cta + 1) : 0;
     if (t1 > t0 && before <= t0 && t0 < before + mine) {
-        // one thread finds the CTA's first place, and has its page ids fetched meanwhile
+        // one thread finds the CTA's first place
         long long at = before;
-        for (int r = r0; r < min(r0 + per, p.B); ++r) {
-            int ctx, rows, start;
-            bool bad;
-            load_request(p, r, ctx, rows, start, bad);
-            if (rows == 0) continue;
+        for (int r = r0;; ++r) {
+            if (per > 1) {                        // else it is what this thread holds already
+                bool bad;
+                load_request(p, r, ctx, rows, start, bad);
+                if (rows == 0) continue;
+            }
             const vplan::Request q{ctx, rows, p.tokens, p.group};
-            const long long n = q.per_head() * p.Hkv;
+            const long long n = per > 1 ? q.per_head() * p.Hkv : mine;
             if (t0 < at + n) {
                 int h, qt, in_unit;
                 place(q, t0 - at, h, qt, in_unit);
-                prefetch_l2(p.pages + static_cast<size_t>(r) * p.max_pages +
-                            min(vplan::tile_at(in_unit, q.tile_places(qt)), q.key_tiles(qt) - 1) *
-                                (kTileKeys / p.ps));
                 ctl.first.b = r, ctl.first.ctx = ctx, ctl.first.rows = rows;
                 ctl.first.start = start, ctl.first.h = h, ctl.first.qt = qt;
                 ctl.first.at = in_unit;
@@ -516,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kWarpK || warp == kWarpV) {
         // ---------------------------------------------------- K or V pages into the ring
-        const int boxes = kTileKeys / p.ps;       // pages of a tile
+        const int boxes = kTileKeys >> p.ps_log2;   // pages of a tile
         const bool is_k = warp == kWarpK;
         const void *map = is_k ? &tm_k : &tm_v;
         const uint32_t full = is_k ? k_full : v_full, empty = is_k ? s_full : o_done;
@@ -529,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int b, h, kt, kt_end, pages;
         };
         auto segment = [&]() {
-            return Seg{w.b, w.h, w.kt, w.kt_end, (w.keys(p) - 1) / p.ps + 1};
+            return Seg{w.b, w.h, w.kt, w.kt_end, ((w.keys(p) - 1) >> p.ps_log2) + 1};
         };
         auto ids_at = [&](const Seg &s, int at) {
             return at + lane < s.pages
@@ -545,11 +559,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (more && ok) {
             const Seg cur = nxt;
             int base = cur.kt * boxes, ids = nids, ids2 = ids_at(cur, base + 32);
-            more = w.next(p);
-            if (more) {
-                nxt = segment();
-                nids = ids_at(nxt, nxt.kt * boxes);
-            }
             for (int kt = cur.kt; kt < cur.kt_end; ++kt) {
                 if (kt * boxes == base + 32) {
                     base += 32;
@@ -585,6 +594,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 ++i;
+                if (kt == cur.kt) {
+                    more = w.next(p);
+                    if (more) {
+                        nxt = segment();
+                        nids = ids_at(nxt, nxt.kt * boxes);
+                    }
+                }
             }
         }
         // copies land before the CTA ends
@@ -879,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             cur.ends = w.kt_end == w.tiles;
             if (cur.starts && !cur.ends)
                 desc = make_int4(cur.row0, cur.h, cur.rows,
-                                 vplan::cta_of(T, w.last_place(p), G) - cta + 1);
+                                 split.cta_of(w.last_place(p)) - cta + 1);
             const int n = (cur.rows + 15) & ~15;
             float *m_row = m_s + seg % C::kMBufs * kN;
             int kt = cur.kt + ((i & 1) == static_cast<uint32_t>(wg) ? 0 : 1);

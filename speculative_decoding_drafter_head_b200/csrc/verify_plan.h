@@ -4,9 +4,9 @@
 // query heads of one key head, against the keys that the tile's last row sees, in key tiles
 // of 128.  All units stand in one line (requests, then key heads, then query tiles), each as
 // kUnitPlaces places, what starting and ending it costs, and then tile_places() a key tile, what
-// a tile costs; a tile belongs to where its first place is.  CTA c of G takes the places from
-// floor(T c / G) to floor(T (c + 1) / G) of the T: equal work whatever the lengths, a function
-// of the lengths alone.  A unit whose tiles are cut by a border is joined from its parts.
+// a tile costs; a tile belongs to where its first place is.  Every CTA takes as many places as
+// the others, to one: equal work whatever the lengths, a function of the lengths alone.  A unit
+// whose tiles are cut by a border is joined from its parts.
 //
 // A tile's cost is its 64 KB and, a little, its rows: tiles of 16 rows took 2430 cycles, of 48
 // 2680 and of 80 2860 where all of them shared the memory's rate.
@@ -69,7 +69,10 @@ struct Request {
     int tokens;        // tokens of a query tile
     int group;         // rows (query heads) of a token
 
-    DSPARK_HD int query_tiles() const { return (rows + tokens - 1) / tokens; }
+    DSPARK_HD int query_tiles() const
+    {
+        return rows <= tokens ? 1 : (rows + tokens - 1) / tokens;
+    }
     // keys that query tile qt sees, and its key tiles
     DSPARK_HD int keys(int qt) const
     {
@@ -98,20 +101,30 @@ struct Request {
     DSPARK_HD long long per_head() const { return before(query_tiles()); }
 };
 
-// first place of CTA c of G
-DSPARK_HD long long first_place(long long T, int c, int G) { return quotient(T * c, G); }
-// the CTA that holds place t
-DSPARK_HD int cta_of(long long T, long long t, int G)
-{
-    return static_cast<int>(quotient((t + 1) * G - 1, T));
-}
-// CTAs that take part: each has as many places as the largest tile at least, so that no CTA
-// between a unit's first and last is without a tile of it
-DSPARK_HD int ctas(long long T, int most)
-{
-    if (T / kMostPlaces >= most) return most;
-    return T < kMostPlaces ? (T > 0) : static_cast<int>(T / kMostPlaces);
-}
+// T places over G CTAs: the first `more` of them take `each` + 1, the others `each`.
+struct Split {
+    long long each, more;
+    int G;
+
+    // Each CTA that takes part has as many places as the largest tile at least, so that no CTA
+    // between a unit's first and last is without a tile of it.
+    DSPARK_HD Split(long long T, int most)
+    {
+        G = T >= static_cast<long long>(most) * kMostPlaces ? most
+            : T < kMostPlaces                               ? (T > 0)
+                                                            : static_cast<int>(T / kMostPlaces);
+        each = G > 0 ? quotient(T, G) : 0;
+        more = T - each * G;
+    }
+    // first place of CTA c
+    DSPARK_HD long long first(int c) const { return each * c + (c < more ? c : more); }
+    // the CTA that holds place t
+    DSPARK_HD int cta_of(long long t) const
+    {
+        const long long cut = (each + 1) * more;
+        return static_cast<int>(t < cut ? quotient(t, each + 1) : more + quotient(t - cut, each));
+    }
+};
 // the first key tile that starts at place `at` of a unit or later
 DSPARK_HD int tile_at(long long at, int tile_places)
 {

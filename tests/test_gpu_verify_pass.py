@@ -232,7 +232,7 @@ def copies(s):
     (33, 33, 7, 7, 128, 96, True, 0, (False, False), 1 << 20),
     (33, 32, 8, 1, 128, 64, False, 200, (True, True), (1 << 31) - 1),
     (17, 17, 6, 2, 128, 0, False, 0, (True, True), 10),
-    (1203, 1190, 16, 4, 128, 128, False, 0, (True, True), 131072),
+    (1203, 1190, 14, 2, 128, 128, False, 0, (True, True), 131072),
     (2001, 1999, 9, 3, 64, 48, True, 0, (True, True), 131072),
     (1500, 2000, 2, 2, 64, 64, False, 0, (True, True), 100),     # the count is clamped
 ])

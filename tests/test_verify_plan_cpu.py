@@ -56,8 +56,10 @@ int main()
             req.push_back(Request{in(0, it % 4 ? 900 : 30000), in(1, 25), tokens, group});
             T += req.back().per_head() * heads;
         }
-        const int G = ctas(T, most);
+        const Split split(T, most);
+        const int G = split.G;
         CHECK(G >= 1 && G <= most && (G == 1 || T / G >= kMostPlaces));
+        CHECK(split.first(0) == 0 && split.first(G) == T);
         // the line, place by place: the unit, and the tile that starts there or -1
         std::vector<int> unit_of, tile_of, tiles;
         for (auto &r : req)
@@ -76,10 +78,10 @@ int main()
         std::vector<std::vector<int>> parts(tiles.size());
         std::vector<int> seen(tiles.size(), 0);
         for (int c = 0; c < G; ++c) {
-            const long long a = first_place(T, c, G), e = first_place(T, c + 1, G);
-            CHECK(a < e && e <= T);
+            const long long a = split.first(c), e = split.first(c + 1);
+            CHECK(a < e && e <= T && e - a >= T / G && e - a <= T / G + 1);
             for (long long t = a; t < e; ++t) {
-                CHECK(cta_of(T, t, G) == c);
+                CHECK(split.cta_of(t) == c);
                 if (tile_of[t] < 0) continue;
                 const int u = unit_of[t];
                 CHECK(tile_of[t] == seen[u]);
