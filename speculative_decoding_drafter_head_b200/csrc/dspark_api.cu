@@ -778,11 +778,15 @@ int dspark_qk_norm_rope_store(const void *qkv, int64_t qkv_stride, const void *q
     prm.slot = slot;
     prm.n_rows = n_rows;
     prm.row_capacity = row_capacity;
-    // warps to a row: as many as keep the SMs busy with the half of the capacity that a batch
-    // fills on average (580 rows: 6.2 us with two, 5.8 with four, 7.0 with eight; 13000 rows:
-    // 65.8 with one, 71.6 with two)
-    const int per_sm = row_capacity / dev->sms;
-    prm.share = per_sm < 1 ? 8 : per_sm < 16 ? 4 : per_sm < 32 ? 2 : 1;
+    // warps to a row: as many as let the half of the capacity that a batch fills on average run
+    // in one wave of CTAs (288 rows of 544: 5.1 us with four, 4.3 with eight; 577 of 1088: 5.6
+    // and 6.6, 7.5 with two; 8000 rows: 37 with one, 38 with two, 47 with four), with more than
+    // one unit of 256 channels each (430 rows of 7 units: 3.4 with four, 4.0 with eight)
+    const int units = ((Hq + 2 * Hkv) * D + 255) / 256;
+    prm.share = Q::kWarps;
+    while (prm.share > 1 && (units <= prm.share || static_cast<long long>(row_capacity) * prm.share >
+                                                       2ll * Q::kWarps * Q::kBlocks * dev->sms))
+        prm.share /= 2;
     prm.Hq = Hq;
     prm.Hkv = Hkv;
     prm.ps = page_size;

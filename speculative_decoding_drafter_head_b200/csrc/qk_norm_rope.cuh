@@ -12,16 +12,18 @@
 // reduced to a fraction of a turn in fp64 before the fp32 sine and cosine: an fp32 product
 // would be off by 2^-24 m radians (0.06 at a position of a million).
 //
-// What bounds it: HBM, every channel read and written once; but 8 channels a lane leave room for
-// some 100 instructions only.  So a lane holds whole rotation pairs (4 channels from each half,
+// What bounds it: HBM, every channel read and written once, which takes some 70 KB on their way
+// to each SM: more than registers hold beside the arithmetic, so channels go to shared memory
+// first (13000 rows of 48 heads of 128: 62 us with two units of 512 bytes ahead in registers,
+// 56 with six in shared memory, 57 with ten, 58 with four).  8 channels a lane leave room for
+// some 100 instructions.  So a lane holds whole rotation pairs (4 channels from each half,
 // or 8 neighbours when interleaved) and needs no exchange for them, and the weights times
 // cosines and sines of its channels stay in registers for all heads of a row:
 //     y_a = inv (w_a c x_a - w_b s x_b),  y_b = inv (w_a s x_a + w_b c x_b)
-// (13000 rows of 48 heads of 128: 104 us with 16-byte chunks, shuffled partners and factors
-// from shared memory).  One warp takes a row, four units of two (D = 128) heads in flight; with
-// few rows the 8 warps of a CTA share one.  Measured (B200, device time): the 13000 rows 62 us,
-// 5.2 TB/s of the 6.47 a copy reaches; 550 rows of the same heads 5.5 us, one row 3.7 us, which
-// are a launch and two dependent loads.
+// (the same rows: 104 us with 16-byte chunks, shuffled partners and factors from shared memory).
+// One warp takes a row, by units of two (D = 128) heads; with few rows up to 8 warps share one.
+// Measured (B200, device time): the 13000 rows 56 us, 5.8 TB/s of the 6.47 a copy reaches; 550
+// rows of the same heads 5.7 us, one row 2.9 us, which are a launch and two dependent loads.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -36,6 +38,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPairs = 64;                     // R / 2 <= 64
 constexpr int kBlocks = 3;                        // CTAs to an SM, at least
 constexpr int kInFlight = 2;                      // units a warp works on at once
+constexpr int kAhead = 3;                         // and so many times that on their way
 
 struct Params {
     const uint16_t *qkv;          // [rows][stride], heads Hq + Hkv + Hkv
@@ -46,7 +49,7 @@ struct Params {
     int rot, interleaved;
     float rope_scale;
     const int32_t *position, *slot, *n_rows;
-    int row_capacity, share;      // warps that share a row: 1 or 8
+    int row_capacity, share;      // warps that share a row: 1, 2, 4 or 8
     int Hq, Hkv, ps, num_pages;
     uint16_t *q_out, *k_cache, *v_cache;
 };
@@ -55,6 +58,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// The lane's four pairs (a_i, b_i) from its channels ca .. ca + 3 and cb .. cb + 3.
+template <bool kInterleaved>
+__device__ __forceinline__ void pairs_of(uint2 x, uint2 y, float (&a)[4], float (&b)[4])
+{
+    const float u[4] = {bf16lo_to_f32(x.x), bf16hi_to_f32(x.x), bf16lo_to_f32(x.y),
+                        bf16hi_to_f32(x.y)};
+    const float v[4] = {bf16lo_to_f32(y.x), bf16hi_to_f32(y.x), bf16lo_to_f32(y.y),
+                        bf16hi_to_f32(y.y)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a[i] = !kInterleaved ? u[i] : i < 2 ? u[2 * i] : v[2 * i - 4];   // neighbours are the pairs
+        b[i] = !kInterleaved ? v[i] : i < 2 ? u[2 * i + 1] : v[2 * i - 3];
+    }
 }
 
 // Factors of a lane's four pairs for queries or keys: y_a = ac x_a - bs x_b, y_b = as x_a + bc x_b.
@@ -68,6 +86,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_store_kernel(c
     constexpr int kLanes = D / 8;                 // lanes of a head
     constexpr int kHeads = 32 / kLanes;           // heads of a unit
     __shared__ float2 turn[kWarps][kMaxPairs];    // (cos, sin) of the CTA's rows
+    __shared__ uint2 ring[kWarps][kAhead][kInFlight][2][32];   // channels, each lane's own
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     launch_dependents();
@@ -91,24 +110,34 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_store_kernel(c
     const uint16_t *from = p.qkv + row * p.stride + ca;
     const int gap = cb - ca, first = (warp - r * p.share) * kHeads;
 
-    // the next units' channels are on their way while these are worked on, the first ones
-    // while the sines are
-    uint2 na[kInFlight], nb[kInFlight];
-    auto fetch = [&](int h0) {
+    // the next units' channels are on their way to shared memory while these are worked on, the
+    // first ones while the sines are; a lane reads what it copied itself, so nobody else waits
+    auto fetch = [&](int u, int at) {
 #pragma unroll
         for (int f = 0; f < kInFlight; ++f) {
-            const int head = h0 + f * step + lane / kLanes;
-            na[f] = nb[f] = make_uint2(0, 0);
+            const int head = u + f * step + lane / kLanes;
             if (head < heads) {
                 const uint16_t *x = from + static_cast<size_t>(head) * D;
-                na[f] = __ldg(reinterpret_cast<const uint2 *>(x));
-                nb[f] = __ldg(reinterpret_cast<const uint2 *>(x + gap));
+                cp_async_8(smem_u32(&ring[warp][at][f][0][lane]), x);
+                cp_async_8(smem_u32(&ring[warp][at][f][1][lane]), x + gap);
             }
         }
+        cp_async_commit();
     };
     int slot = -1;
+    uint2 wq[2], wk[2];                           // weights of the lane's channels, or ones
+    wq[0] = wq[1] = wk[0] = wk[1] = make_uint2(0x3F803F80u, 0x3F803F80u);
     if (live) {
-        fetch(first);
+        if (p.q_weight) {
+            wq[0] = __ldg(reinterpret_cast<const uint2 *>(p.q_weight + ca));
+            wq[1] = __ldg(reinterpret_cast<const uint2 *>(p.q_weight + cb));
+        }
+        if (p.k_weight) {
+            wk[0] = __ldg(reinterpret_cast<const uint2 *>(p.k_weight + ca));
+            wk[1] = __ldg(reinterpret_cast<const uint2 *>(p.k_weight + cb));
+        }
+#pragma unroll
+        for (int at = 0; at < kAhead; ++at) fetch(first + at * kInFlight * step, at);
         slot = p.slot[row];
     }
     for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
@@ -124,49 +153,41 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_store_kernel(c
     if (!live) return;
 
     Factors fq, fk;
+    float qa[4], qb[4], ka[4], kb[4];
+    pairs_of<kInterleaved>(wq[0], wq[1], qa, qb);
+    pairs_of<kInterleaved>(wk[0], wk[1], ka, kb);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int xa = kInterleaved ? 8 * sub + 2 * i : ca + i;
-        const int xb = kInterleaved ? xa + 1 : cb + i;
-        float2 t = make_float2(1.0f, 0.0f);
-        if (turns) t = turn[r][kInterleaved ? xa / 2 : xa];
-        auto weight = [](const uint16_t *w, int ch) {
-            return w ? __uint_as_float(static_cast<uint32_t>(__ldg(w + ch)) << 16) : 1.0f;
-        };
-        const float qa = weight(p.q_weight, xa), qb = weight(p.q_weight, xb);
-        const float ka = weight(p.k_weight, xa), kb = weight(p.k_weight, xb);
-        fq.ac[i] = qa * t.x, fq.bs[i] = qb * t.y, fq.as[i] = qa * t.y, fq.bc[i] = qb * t.x;
-        fk.ac[i] = ka * t.x, fk.bs[i] = kb * t.y, fk.as[i] = ka * t.y, fk.bc[i] = kb * t.x;
+        const float2 t = turns ? turn[r][4 * sub + i] : make_float2(1.0f, 0.0f);
+        fq.ac[i] = qa[i] * t.x, fq.bs[i] = qb[i] * t.y, fq.as[i] = qa[i] * t.y, fq.bc[i] = qb[i] * t.x;
+        fk.ac[i] = ka[i] * t.x, fk.bs[i] = kb[i] * t.y, fk.as[i] = ka[i] * t.y, fk.bc[i] = kb[i] * t.x;
     }
     const int page = slot / p.ps;
     const bool stored = slot >= 0 && page < p.num_pages;
     if (!stored && lane == 0) record_error(DSPARK_INVALID_PAGE);
     const size_t place =
         stored ? (static_cast<size_t>(page) * p.Hkv * p.ps + (slot - page * p.ps)) * D : 0;
+    int at = 0;
     for (int u0 = first; u0 < heads; u0 += kInFlight * step) {
         const int h0 = u0 + lane / kLanes;
         uint2 xa[kInFlight], xb[kInFlight];
+        cp_async_wait<kAhead - 1>();
 #pragma unroll
-        for (int f = 0; f < kInFlight; ++f) xa[f] = na[f], xb[f] = nb[f];
-        fetch(u0 + kInFlight * step);
+        for (int f = 0; f < kInFlight; ++f)
+            xa[f] = ring[warp][at][f][0][lane], xb[f] = ring[warp][at][f][1][lane];
+        fetch(u0 + kAhead * kInFlight * step, at);
+        if (++at == kAhead) at = 0;
 #pragma unroll
         for (int f = 0; f < kInFlight; ++f) {
             const int head = h0 + f * step;
             if (u0 + f * step >= heads) break;
-            float a[4] = {bf16lo_to_f32(xa[f].x), bf16hi_to_f32(xa[f].x), bf16lo_to_f32(xa[f].y),
-                          bf16hi_to_f32(xa[f].y)};
-            float b[4] = {bf16lo_to_f32(xb[f].x), bf16hi_to_f32(xb[f].x), bf16lo_to_f32(xb[f].y),
-                          bf16hi_to_f32(xb[f].y)};
+            float a[4], b[4];
+            pairs_of<kInterleaved>(xa[f], xb[f], a, b);
             float sq = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) sq = fmaf(a[i], a[i], fmaf(b[i], b[i], sq));
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
-            if (kInterleaved) {                   // neighbours are the pairs
-                const float t0 = a[1], t1 = a[3], t2 = b[0], t3 = b[2];
-                a[1] = a[2], a[2] = t2, a[3] = t3;
-                b[0] = t0, b[2] = b[1], b[1] = t1;
-            }
             uint2 ya = xa[f], yb = xb[f];
             // queries or keys; values stay as they are
             auto turned = [&](const Factors &w, bool normed) {
