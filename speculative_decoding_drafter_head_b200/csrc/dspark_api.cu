@@ -907,8 +907,9 @@ int dspark_verify_attention(const void *q, const void *k_cache, const void *v_ca
     const int grid = dev->sms < A::kMaxCtas ? dev->sms : A::kMaxCtas;
     if (int st = launch_overlapped(kern, dim3(grid), A::kThreads, smem, 1, stream, tm_k, tm_v, prm))
         return st;
+    const int split = (wide ? A::kMaxRows : 64) / (2 * (A::kJoinThreads / 32));
     return launch_overlapped(D == 64 ? A::verify_join_kernel<64> : A::verify_join_kernel<128>,
-                             dim3(grid, A::kJoinSplit), A::kJoinThreads, 0, 1, stream, prm);
+                             dim3(grid, split), A::kJoinThreads, 0, 1, stream, prm);
 }
 
 size_t dspark_sts_fit_workspace_bytes(int N, int gamma, int n_t, int n_bins)

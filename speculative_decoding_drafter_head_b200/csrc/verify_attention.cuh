@@ -70,7 +70,6 @@ constexpr float kRaise = 24.0f;                   // log2 of the weight at which
 constexpr float kUnset = -1e30f;                  // m of a row that has met no finite score yet
 constexpr int kOnesBytes = 1152;                  // 8 x 2 core matrices of 128 B, one apart
 constexpr int kJoinThreads = 256;
-constexpr int kJoinSplit = 4;                     // CTAs that share a unit's rows
 constexpr int kJoinAhead = 8;                     // parts whose O a row has in flight
 
 struct Params {
@@ -1073,10 +1072,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Adds up the parts of the unit that starts in CTA blockIdx.x and ends in a later one: with
 // M = max m over the parts,  out = sum 2^(m - M) O / sum 2^(m - M) l.  What bounds it: latency, of
-// three loads that need one another if nothing is done about it.  So every row has a warp of its
-// own (kJoinSplit CTAs to a unit), lane i holds part i's (m, l), and O is fetched beside them.
-// Added up by one CTA of 16 warps a unit, the parts of the benchmark's long request took
-// 15 us after the attention's last CTA.
+// three loads that need one another if nothing is done about it.  So two rows at most have a warp
+// of their own (gridDim.y CTAs to a unit; 17 tokens of 4 heads over 131 thousand keys: 96.6 us a
+// call with one, 93.1 with two, 91.8 with four, 89.9 with six or more), lane i holds part i's
+// (m, l), and O is fetched beside them.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) verify_join_kernel(const Params p)
 {
@@ -1088,7 +1087,7 @@ __global__ void __launch_bounds__(kJoinThreads) verify_join_kernel(const Params 
     if (parts < 2) return;
     const int lane = threadIdx.x & 31;
     for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
-         r += kJoinSplit * (kJoinThreads / 32)) {
+         r += gridDim.y * (kJoinThreads / 32)) {
         // part 0 is its CTA's last, the others their CTAs' first
         auto part = [&](int i) {
             return static_cast<size_t>(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kMaxRows + r;
