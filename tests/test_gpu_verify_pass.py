@@ -234,6 +234,8 @@ def copies(s):
     (17, 17, 6, 2, 128, 0, False, 0, (True, True), 10),
     (1203, 1190, 14, 2, 128, 128, False, 0, (True, True), 131072),
     (2001, 1999, 9, 3, 64, 48, True, 0, (True, True), 131072),
+    (1901, 1877, 25, 3, 128, 96, True, 0, (True, True), 131072),   # two warps to a row
+    (3701, 3655, 13, 5, 128, 128, False, 8, (True, False), 131072),   # and one
     (1500, 2000, 2, 2, 64, 64, False, 0, (True, True), 100),     # the count is clamped
 ])
 def test_norm_rope_store(ds, cap, n, Hq, Hkv, D, rot, interleaved, gap, weights, far):
