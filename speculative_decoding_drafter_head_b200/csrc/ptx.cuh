@@ -499,7 +499,8 @@ __device__ __forceinline__ void launch_dependents()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Waits until the kernels before this one have finished and their writes can be read.
+// Waits until the kernels before this one have finished and their writes can be read; with plain
+// loads, since a read-only one (__ldg) may be taken to hold for all of this kernel and moved up.
 __device__ __forceinline__ void wait_for_prior_kernels()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -129,12 +129,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_store_kernel(c
     wq[0] = wq[1] = wk[0] = wk[1] = make_uint2(0x3F803F80u, 0x3F803F80u);
     if (live) {
         if (p.q_weight) {
-            wq[0] = __ldg(reinterpret_cast<const uint2 *>(p.q_weight + ca));
-            wq[1] = __ldg(reinterpret_cast<const uint2 *>(p.q_weight + cb));
+            wq[0] = *reinterpret_cast<const uint2 *>(p.q_weight + ca);
+            wq[1] = *reinterpret_cast<const uint2 *>(p.q_weight + cb);
         }
         if (p.k_weight) {
-            wk[0] = __ldg(reinterpret_cast<const uint2 *>(p.k_weight + ca));
-            wk[1] = __ldg(reinterpret_cast<const uint2 *>(p.k_weight + cb));
+            wk[0] = *reinterpret_cast<const uint2 *>(p.k_weight + ca);
+            wk[1] = *reinterpret_cast<const uint2 *>(p.k_weight + cb);
         }
 #pragma unroll
         for (int at = 0; at < kAhead; ++at) fetch(first + at * kInFlight * step, at);

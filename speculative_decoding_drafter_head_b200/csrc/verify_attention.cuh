@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto ids_at = [&](const Seg &s, int at) {
             return at + lane < s.pages
-                       ? __ldg(p.pages + static_cast<size_t>(s.b) * p.max_pages + at + lane)
+                       ? p.pages[static_cast<size_t>(s.b) * p.max_pages + at + lane]
                        : 0;
         };
         Seg nxt = {};
