@@ -66,6 +66,7 @@ constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpQ = 11;
 constexpr int kQThreads = 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWaitHintNs = 20000;
+constexpr int kLooks = 4096;                      // at two barriers in turn, before a wait for one
 constexpr float kRaise = 24.0f;                   // log2 of the weight at which m rises
 constexpr float kUnset = -1e30f;                  // m of a row that has met no finite score yet
 constexpr int kOnesBytes = 1152;                  // 8 x 2 core matrices of 128 B, one apart
@@ -76,6 +77,7 @@ struct Params {
     const uint16_t *q, *k_cache, *v_cache;
     const int32_t *pages, *context, *row_start;
     int B, row_capacity, Hq, Hkv, group, tokens, ps, ps_log2, max_pages, num_pages;
+    uint32_t group_inv;                           // r / group = r group_inv >> 16, r < 112
     float scale_log2;                             // scale log2(e)
     uint16_t *out;
     int4 *desc;                                   // [ctas] the unit that starts a join
@@ -224,6 +226,7 @@ struct Walk {
     int base, l_ctx, l_rows, l_start;             // request base + lane
     int b, ctx, rows, start;
     int h, qt, kt, kt_end, tiles;                 // segment [kt, kt_end) of the unit's tiles
+    int all;                                      // places of the unit
     long long left, unit;                         // places left, and the first of the unit
 
     __device__ __forceinline__ void load(const Params &p)
@@ -249,11 +252,16 @@ struct Walk {
     {
         const vplan::Request r = request(p);
         tiles = r.key_tiles(qt);
-        const int per = r.tile_places(qt), all = vplan::kUnitPlaces + tiles * per;
-        const int n = static_cast<int>(min(static_cast<long long>(all - at), left));
-        left -= n;
+        const int per = r.tile_places(qt);
+        all = vplan::kUnitPlaces + tiles * per;
         kt = vplan::tile_at(at, per);
-        kt_end = min(vplan::tile_at(at + n, per), tiles);
+        if (all - at <= left) {
+            left -= all - at;
+            kt_end = tiles;
+        } else {
+            kt_end = min(vplan::tile_at(at + left, per), tiles);
+            left = 0;
+        }
         return kt_end > kt;
     }
     __device__ __forceinline__ long long last_place(const Params &p) const
@@ -276,7 +284,7 @@ struct Walk {
     __device__ __forceinline__ bool next(const Params &p)
     {
         if (left <= 0) return false;
-        unit += vplan::kUnitPlaces + static_cast<long long>(tiles) * request(p).tile_places(qt);
+        unit += all;
         if (++qt == request(p).query_tiles()) {
             qt = 0;
             if (++h == p.Hkv) {
@@ -630,6 +638,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t i = 0, slot = 0, j = 0, jslot = 0, jbuf = 0;
             bool ok = true;
             auto weights_there = [&]() { return wait(p_full + 8 * (j & 1), (j >> 1) & 1u, ctl, p); };
+            auto values_ready = [&]() {
+                return mbar_test_wait(p_full + 8 * (j & 1), (j >> 1) & 1u) &&
+                       mbar_test_wait(tile_bar(v_full, j), tile_phase(j)) &&
+                       (!t0.first || mbar_test_wait(o_empty + 8 * (t0.seg % C::kOBufs),
+                                                    ((t0.seg / C::kOBufs) & 1u) ^ 1u));
+            };
             auto values = [&]() {
                 const uint32_t ob = t0.seg % C::kOBufs;
                 ok = wait(tile_bar(v_full, j), tile_phase(j), ctl, p) &&
@@ -656,7 +670,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t seg = 0; ok; ++seg) {
                 const uint32_t qb = seg % C::kQBufs;
                 const uint32_t turn = (seg / C::kQBufs) & 1u;
-                while (ok && ahead > 0 && !mbar_test_wait(q_full + 8 * qb, turn)) {
+                // values or queries, whichever are there first (a bounded wait after so many looks)
+                for (int looks = 0; ok && ahead > 0 && !mbar_test_wait(q_full + 8 * qb, turn);) {
+                    if (++looks < kLooks && !values_ready()) continue;
+                    looks = 0;
                     ok = weights_there();
                     if (ok) values();
                 }
@@ -716,15 +733,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 static_cast<size_t>(w.h) * p.group;
             constexpr int kStep = kQThreads / (D / 8);   // rows between a thread's
             const int u = t % (D / 8);
-            int i = t / (D / 8) / p.group, g = t / (D / 8) - i * p.group;
+            const uint16_t *from = p.q + row0 * D + u * 8;
+            const long long token = static_cast<long long>(p.Hq - p.group) * D;   // past a token's rows
+#pragma unroll 4
             for (int r = t / (D / 8); r < n; r += kStep) {
                 const uint32_t to = dst + (u >> 3) * (kN * 128) + r * 128 +
                                     (((u & 7) ^ (r & 7)) << 4);
                 if (r < rows)
-                    cp_async_16(to, p.q + (row0 + static_cast<size_t>(i) * p.Hq + g) * D + u * 8);
+                    cp_async_16(to, from + r * D + (r * p.group_inv >> 16) * token);
                 else
                     sts128(to, 0, 0, 0, 0);
-                for (g += kStep; g >= p.group; g -= p.group) ++i;
             }
             cp_async_wait_all();
             fence_proxy_async_smem();
@@ -788,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (at < s.rows) {
                 const float l = red[at];
                 if (direct) {
-                    const int i = at / p.group;
+                    const int i = at * p.group_inv >> 16;
                     red[kN + at] = __int_as_float(i * p.Hq + at - i * p.group);
                     red[at] = 1.0f / l;
                 } else {
