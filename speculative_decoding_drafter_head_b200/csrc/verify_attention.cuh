@@ -934,36 +934,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!first) await(m_full + 8 * (seg & 1), (seg >> 1) & 1u);
                 __syncwarp();
                 tc_fence_after();
-                if (masked) {
-                    // values behind the last key, and those that are not finite
-                    const uint32_t slot = i % C::kSlots;
-                    await(tile_bar(v_full, i), tile_phase(i));
-                    // 16-byte chunks in an order of the lane's own, so that neighbouring rows,
-                    // 128 bytes apart, meet different banks
-                    const uint32_t v = s0 + C::kRingV + slot * C::kTileBytes + at * 128;
-                    auto chunk = [&](int u) {
-                        return v + (u >> 3) * C::kHalfBytes + (((u ^ at) & 7) << 4);
-                    };
-                    if (key >= cur.keys) {
-#pragma unroll
-                        for (int u = 0; u < D / 8; ++u) sts128(chunk(u), 0, 0, 0, 0);
-                    } else if (from > 0) {
-                        bool odd = false;
-#pragma unroll 4
-                        for (int u = 0; u < D / 8; ++u) {
-                            uint32_t x0, x1, x2, x3;
-                            lds128(chunk(u), x0, x1, x2, x3);
-                            if (not_finite(x0) || not_finite(x1) || not_finite(x2) ||
-                                not_finite(x3)) {
-                                odd = true;
-                                sts128(chunk(u), finite_or_zero(x0), finite_or_zero(x1),
-                                       finite_or_zero(x2), finite_or_zero(x3));
-                            }
-                        }
-                        if (odd) *reinterpret_cast<volatile int *>(&ctl.odd[seg % C::kMBufs]) = 1;
-                    }
-                    __syncwarp();
-                }
                 // With three P buffers this one is free: its last product, three tiles ago, came
                 // before this S in the tensor core's order.  With two it is waited for.
                 const uint32_t prow = s0 + C::kP + i % C::kPBufs * C::kPBytes + at * 128;
@@ -1051,6 +1021,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int u = (c >> 3) & 7;
                         sts128(to + ((u ^ (at & 7)) << 4), word[0], word[1], word[2], word[3]);
                         sts128(to + (((u + 1) ^ (at & 7)) << 4), word[4], word[5], word[6], word[7]);
+                    }
+                    if (masked && tries == 0) {
+                        // values behind the last key, and those that are not finite: the last
+                        // thing, since the values come after the keys
+                        const uint32_t slot = i % C::kSlots;
+                        await(tile_bar(v_full, i), tile_phase(i));
+                        // 16-byte chunks in an order of the lane's own, so that neighbouring rows,
+                        // 128 bytes apart, meet different banks
+                        const uint32_t v = s0 + C::kRingV + slot * C::kTileBytes + at * 128;
+                        auto chunk = [&](int u) {
+                            return v + (u >> 3) * C::kHalfBytes + (((u ^ at) & 7) << 4);
+                        };
+                        if (key >= cur.keys) {
+#pragma unroll
+                            for (int u = 0; u < D / 8; ++u) sts128(chunk(u), 0, 0, 0, 0);
+                        } else if (from > 0) {
+                            bool odd = false;
+#pragma unroll 4
+                            for (int u = 0; u < D / 8; ++u) {
+                                uint32_t x0, x1, x2, x3;
+                                lds128(chunk(u), x0, x1, x2, x3);
+                                if (not_finite(x0) || not_finite(x1) || not_finite(x2) ||
+                                    not_finite(x3)) {
+                                    odd = true;
+                                    sts128(chunk(u), finite_or_zero(x0), finite_or_zero(x1),
+                                           finite_or_zero(x2), finite_or_zero(x3));
+                                }
+                            }
+                            if (odd) *reinterpret_cast<volatile int *>(&ctl.odd[seg % C::kMBufs]) = 1;
+                        }
                     }
                     // this tile's turn, and what has become of m
                     if (i > 0) await(before, before_phase);
