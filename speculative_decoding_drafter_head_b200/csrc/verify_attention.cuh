@@ -403,9 +403,10 @@ __device__ __forceinline__ float column_max(float (&v)[16])
     return fmaxf(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
 }
 
-__device__ __forceinline__ bool not_finite(uint32_t w)   // either bf16 of a word
+// sum += 0 x, of two bf16 each: NaN from a value that is not finite on, else zero
+__device__ __forceinline__ void add_zero_times(uint32_t &sum, uint32_t x)
 {
-    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(x), "r"(0u));
 }
 __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w)
 {
@@ -816,10 +817,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             group_sync(wg);
             const size_t row0 = static_cast<size_t>(s.row0) * p.Hq + static_cast<size_t>(s.h) * p.group;
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(lane_base + C::kColO + ob * kN, o);
             for (int c0 = 0; c0 < s.rows; c0 += 16) {
-                uint32_t o[16];
                 float v[16];
-                tmem_ld_32x32b_x16(lane_base + C::kColO + ob * kN + c0, o);
                 tmem_wait_ld16(o);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -830,6 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v[4 * q + 2] = __uint_as_float(o[4 * q + 2]) * f.z;
                     v[4 * q + 3] = __uint_as_float(o[4 * q + 3]) * f.w;
                 }
+                if (c0 + 16 < s.rows) tmem_ld_32x32b_x16(lane_base + C::kColO + ob * kN + c0 + 16, o);
                 if (odd && has_d) {               // values that are not finite, to who sees them
                     for (int j = max(s.kt * kTileKeys, s.hidden);
                          j < min(s.kt_end * kTileKeys, s.keys); ++j) {
@@ -1037,19 +1039,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int u = 0; u < D / 8; ++u) sts128(chunk(u), 0, 0, 0, 0);
                         } else if (from > 0) {
-                            bool odd = false;
-#pragma unroll 4
+                            uint32_t sum[4] = {};          // of zero times each value
+#pragma unroll
                             for (int u = 0; u < D / 8; ++u) {
-                                uint32_t x0, x1, x2, x3;
-                                lds128(chunk(u), x0, x1, x2, x3);
-                                if (not_finite(x0) || not_finite(x1) || not_finite(x2) ||
-                                    not_finite(x3)) {
-                                    odd = true;
+                                uint32_t x[4];
+                                lds128(chunk(u), x[0], x[1], x[2], x[3]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) add_zero_times(sum[e], x[e]);
+                            }
+                            if (((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7FFF7FFFu) != 0) {
+#pragma unroll 1
+                                for (int u = 0; u < D / 8; ++u) {
+                                    uint32_t x0, x1, x2, x3;
+                                    lds128(chunk(u), x0, x1, x2, x3);
                                     sts128(chunk(u), finite_or_zero(x0), finite_or_zero(x1),
                                            finite_or_zero(x2), finite_or_zero(x3));
                                 }
+                                *reinterpret_cast<volatile int *>(&ctl.odd[seg % C::kMBufs]) = 1;
                             }
-                            if (odd) *reinterpret_cast<volatile int *>(&ctl.odd[seg % C::kMBufs]) = 1;
                         }
                     }
                     // this tile's turn, and what has become of m
