@@ -43,7 +43,9 @@
 // Measured (B200, device time): 64 requests, 32/8 heads of 128, 500-8000 keys, up to 17 rows
 // each 178 us, 6.2 TB/s of the 6.47 a copy reaches; 256 requests of one row, 32/4 heads 305 us,
 // 6.7 TB/s; one request of 131 thousand keys 90 us, 6.0 TB/s; one token over 700 keys 10 us, of which
-// 5 go before the first tile has come (launch, lengths, this CTA's share, page ids, the tile).
+// 4 go before the first tile has come (launch, lengths, this CTA's share, page ids, the tile).
+// With few keys to a unit its start and end are the bound: 2 us a unit of one tile and 4 rows,
+// 2.6 of 32, 5.4 of 112 (Q in, the reference, the output), which overlap the other group's.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
