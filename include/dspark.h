@@ -231,6 +231,20 @@ int dspark_verify_prefix(const int32_t *x, const int32_t *L, const int32_t *targ
                          dspark_stream_t stream);
 
 /*
+ * The same after dspark_verify_layout, which may cut a request's rows where pages run out, down
+ * to none: only target tokens that a row of the step computed count.
+ *   rows [B] int32 as the layout wrote them;  anchor [B] int32 as the layout read it
+ *   rows[b] >= 1: as dspark_verify_prefix with the length min(L[b], rows[b] - 1)
+ *   rows[b] < 1 (an idle slot, or a request that got no page):  accepted_out[b] = -1, which adds
+ *   nothing to the context, and bonus_out[b] = anchor[b], the token to send again
+ * target [B, gamma + 1] need hold nothing behind a request's rows.  bonus_out may be anchor.
+ * gamma may be 0 (decoding without drafts; x is not read then).
+ */
+int dspark_verify_prefix_rows(const int32_t *x, const int32_t *L, const int32_t *rows,
+                              const int32_t *anchor, const int32_t *target, int B, int gamma,
+                              int32_t *accepted_out, int32_t *bonus_out, dspark_stream_t stream);
+
+/*
  * Sequential Temperature Scaling: fitting the per-position temperatures T [gamma]
  * that dspark_confidence_sts divides the confidence logits by.
  * [G] section 5 "Sequential Temperature Scaling": the joint (survival) probability is
@@ -300,7 +314,7 @@ int dspark_schedule_prefix_noalloc(const float *P, int B, int gamma, const doubl
 /*
  * The target's verification pass: the ragged batch that schedule_prefix's lengths call for,
  * over a paged key-value cache.  (No counterpart on the DSpark pages, which take the target
- * model as given: these calls join dspark_schedule_prefix to dspark_verify_prefix on the
+ * model as given: these calls join dspark_schedule_prefix to dspark_verify_prefix_rows on the
  * device, without the host knowing a length.)
  *
  * A cache has num_pages pages of page_size tokens; per layer the keys and the values are
@@ -326,10 +340,11 @@ int dspark_schedule_prefix_noalloc(const float *P, int B, int gamma, const doubl
  * place, but for context, which changes only with
  *   accepted [B] int32 or null: context[b] += min(accepted[b] + 1, rows[b]) comes first, with
  *                       rows the output of the preceding call: the last step's tokens that
- *                       stuck (accepted as dspark_verify_prefix wrote it; -1 adds none)
+ *                       stuck (accepted as dspark_verify_prefix_rows wrote it; -1 adds none)
  * Rows of request b: n_b = L[b] + 1, or fewer where the free pages or the block table ran
- * out; then L[b] becomes max(n_b - 1, 0) (verification stays lossless with any lengths) and
- * DSPARK_OUT_OF_PAGES is recorded.
+ * out; then L[b] becomes max(n_b - 1, 0) and DSPARK_OUT_OF_PAGES is recorded.  Verification
+ * stays lossless with any number of rows from one on; a request of none has L[b] = 0 as well, so
+ * that its rows[b] = 0 has to be looked at: dspark_verify_prefix_rows does.
  *   rows [B], row_start [B + 1] int32   n_b, and its running sum from 0
  * and for row r = row_start[b] + i, 0 <= i < n_b:
  *   position [row_capacity] int32   context[b] + i

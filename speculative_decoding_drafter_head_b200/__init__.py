@@ -48,7 +48,7 @@ EXPORTED = (
     "dspark_sts_fit_workspace_bytes", "dspark_sts_fit", "dspark_draft_step_rnn",
     "dspark_draft_confidence_step", "dspark_step", "dspark_verify_layout",
     "dspark_qk_norm_rope_store", "dspark_verify_attention_workspace_bytes",
-    "dspark_verify_attention",
+    "dspark_verify_attention", "dspark_verify_prefix_rows",
 )
 
 _lib = None
@@ -86,6 +86,7 @@ def load(build_if_missing: bool = True):
                                 p, p, p, p, p, p, p, p, p, p, sz, p]
     lib.dspark_schedule_prefix.argtypes = [p, i, i, p, p, p, p, p, sz, p]
     lib.dspark_verify_prefix.argtypes = [p, p, p, i, i, p, p, p]
+    lib.dspark_verify_prefix_rows.argtypes = [p, p, p, p, p, i, i, p, p, p]
     lib.dspark_verify_layout.argtypes = [p] * 10 + [i] * 6 + [p] * 5
     lib.dspark_qk_norm_rope_store.argtypes = [p, C.c_int64, p, p, f32, p, i, i, f32, p, p, p, i, i,
                                               i, i, i, i, p, p, p, p]
@@ -238,10 +239,28 @@ def schedule_prefix(P, Tstep_us, L_out, N_out, objective_out, workspace, stream=
     _check("dspark_schedule_prefix", st)
 
 
-def verify_prefix(x, L, target, accepted_out, bonus_out, stream=None):
-    """Strict prefix-match verification (see dspark_verify_prefix)."""
+def verify_prefix(x, L, target, accepted_out, bonus_out, stream=None, rows=None, anchor=None):
+    """Strict prefix-match verification (see dspark_verify_prefix).
+
+    rows, anchor [B] int32: after verify_layout, so that a request without rows in this step
+    accepts -1 drafts and keeps its anchor (see dspark_verify_prefix_rows)."""
     import torch
     B, gamma = x.shape
+    if (rows is None) != (anchor is None):
+        raise ValueError("rows and anchor go together")
+    if rows is not None:
+        for name, t, shape in (("L", L, (B,)), ("rows", rows, (B,)), ("anchor", anchor, (B,)),
+                               ("target", target, (B, gamma + 1)),
+                               ("accepted_out", accepted_out, (B,)), ("bonus_out", bonus_out, (B,))):
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        st = load().dspark_verify_prefix_rows(
+            _dev(x, torch.int32, "x"), _dev(L, torch.int32, "L"), _dev(rows, torch.int32, "rows"),
+            _dev(anchor, torch.int32, "anchor"), _dev(target, torch.int32, "target"), B, gamma,
+            _dev(accepted_out, torch.int32, "accepted_out"),
+            _dev(bonus_out, torch.int32, "bonus_out"), _stream(stream))
+        _check("dspark_verify_prefix_rows", st)
+        return
     st = load().dspark_verify_prefix(
         _dev(x, torch.int32, "x"), _dev(L, torch.int32, "L"), _dev(target, torch.int32, "target"),
         B, gamma, _dev(accepted_out, torch.int32, "accepted_out"),

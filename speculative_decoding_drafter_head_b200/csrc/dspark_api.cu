@@ -676,6 +676,25 @@ int dspark_verify_prefix(const int32_t *x, const int32_t *L, const int32_t *targ
     return from_cuda(cudaGetLastError());
 }
 
+int dspark_verify_prefix_rows(const int32_t *x, const int32_t *L, const int32_t *rows,
+                              const int32_t *anchor, const int32_t *target, int B, int gamma,
+                              int32_t *accepted_out, int32_t *bonus_out, dspark_stream_t stream)
+{
+    namespace Vf = dspark::verify;
+    if ((!x && gamma > 0) || !L || !rows || !anchor || !target || !accepted_out || !bonus_out)
+        return DSPARK_INVALID_ARG;
+    if (!aligned(x, 4) || !aligned(L, 4) || !aligned(rows, 4) || !aligned(anchor, 4) ||
+        !aligned(target, 4) || !aligned(accepted_out, 4) || !aligned(bonus_out, 4))
+        return DSPARK_INVALID_ARG;
+    if (B < 1 || gamma < 0 || gamma > 4096) return DSPARK_UNSUPPORTED_SHAPE;
+    DeviceInfo *dev = nullptr;
+    if (int st = current_device(&dev)) return st;
+    Vf::verify_prefix_rows_kernel<<<(B + Vf::kThreads - 1) / Vf::kThreads, Vf::kThreads, 0,
+                                    stream>>>(x, L, rows, anchor, target, B, gamma, accepted_out,
+                                              bonus_out);
+    return from_cuda(cudaGetLastError());
+}
+
 int dspark_verify_layout(int32_t *L, const int32_t *anchor, const int32_t *x,
                          const int32_t *accepted, int32_t *context, int32_t *rows, int32_t *pages,
                          int32_t *held, int32_t *free_pages, int32_t *free_count, int B, int gamma,

@@ -66,5 +66,25 @@ __global__ void __launch_bounds__(kThreads)
     verify_request(x, L, target, b, gamma, accepted_out, bonus_out);
 }
 
+// The same behind a batch layout, which may give a request fewer rows than its length asks for,
+// or none: a target token that no row of the step computed is not looked at.  anchor and
+// bonus_out may be one array.
+__global__ void __launch_bounds__(kThreads)
+    verify_prefix_rows_kernel(const int32_t *__restrict__ x, const int32_t *__restrict__ L,
+                              const int32_t *__restrict__ rows, const int32_t *anchor,
+                              const int32_t *__restrict__ target, int B, int gamma,
+                              int32_t *__restrict__ accepted_out, int32_t *bonus_out)
+{
+    const int b = blockIdx.x * kThreads + threadIdx.x;
+    if (b >= B) return;
+    const int n = rows[b];
+    if (n < 1) {
+        accepted_out[b] = -1;
+        bonus_out[b] = anchor[b];
+        return;
+    }
+    verify_request_len(x, min(L[b], n - 1), target, b, gamma, accepted_out, bonus_out);
+}
+
 }  // namespace verify
 }  // namespace dspark

@@ -36,7 +36,7 @@ buffers of one step's ragged batch.  A step is
     vp.layout(L, anchor, x, accepted)                 # batch of this step, pages, slots
     for layer in range(layers):                       # the target's own products around it
         out = vp.attend(layer, qkv(layer), q_weight, k_weight)
-    verify_prefix(x, L, target, accepted, bonus)
+    vp.verify(L, anchor, x, target, accepted, bonus)  # bonus: the next step's anchor
 
 with every length on the device, so the whole step can be captured as one CUDA graph.
 
@@ -45,7 +45,7 @@ This module only orders launches of the library's kernels; it computes nothing.
 from __future__ import annotations
 
 from . import (qk_norm_rope_store, schedule_prefix, verify_attention,
-               verify_attention_workspace_bytes, verify_layout, workspace_bytes)
+               verify_attention_workspace_bytes, verify_layout, verify_prefix, workspace_bytes)
 
 
 def scores_slot(t: int, lag: int) -> int:
@@ -128,7 +128,15 @@ class LaggedScheduler:
 
 
 class VerifyPass:
-    """Paged cache, block tables and batch buffers of the target's verification pass."""
+    """Paged cache, block tables and batch buffers of the target's verification pass.
+
+    All slots start idle.  Between steps the caller starts a request by context[b] = 0 and
+    accepted[b] = -1 (nothing of the slot's last request sticks), its first token as anchor[b],
+    and ends one by context[b] = -1: the next layout takes its pages back.  A prompt goes in by
+    pieces of up to gamma + 1 tokens, a step each: the piece's first token as anchor[b], the others
+    in x[b], L[b] their number, and accepted[b] = L[b] for the layout after it; context[b] says how
+    far it has come.  Where pages run out a request gets fewer rows, or none (rows[b] = 0), and
+    has to be sent again: verify() sees to it in the steps that verify."""
 
     def __init__(self, B: int, gamma: int, layers: int, Hq: int, Hkv: int, D: int, page_size: int,
                  num_pages: int, max_pages: int, inv_freq=None, interleaved: bool = False,
@@ -164,6 +172,13 @@ class VerifyPass:
                       self.free_count, self.row_start, self.position, self.slot, self.page_size,
                       self.gamma, anchor=anchor, x=x, token=self.token, accepted=accepted,
                       stream=stream)
+
+    def verify(self, L, anchor, x, target, accepted_out, bonus_out, stream=None):
+        """Verification of the step that layout() laid out, by its rows: a request without rows
+        accepts -1 drafts and keeps its anchor as bonus token (see dspark_verify_prefix_rows).
+        target [B, gamma + 1]: row row_start[b] + i's token at [b, i]."""
+        verify_prefix(x, L, target, accepted_out, bonus_out, stream=stream, rows=self.rows,
+                      anchor=anchor)
 
     def attend(self, layer: int, qkv, q_weight=None, k_weight=None, stream=None):
         """One layer's attention of the batch: qkv [B (gamma + 1), (Hq + 2 Hkv) D] normalised,
