@@ -429,7 +429,8 @@ int dspark_set_wait_timeout_ns(uint64_t ns);
 
 /* Test hook: the draft kernel's grid barrier waits for `extra` more arrivals than
  * there are CTAs, and the verification attention's tiles for as many more than there are
- * threads, so that their bounded waits run out (0 restores normal use). */
+ * threads, so that their bounded waits run out; the batch layout is launched without its
+ * cluster, so that a grid of several CTAs reports DSPARK_BAD_LAUNCH (0 restores normal use). */
 int dspark_debug_barrier_extra(int extra);
 
 #ifdef __cplusplus

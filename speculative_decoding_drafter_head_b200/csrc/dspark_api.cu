@@ -758,7 +758,8 @@ int dspark_verify_layout(int32_t *L, const int32_t *anchor, const int32_t *x,
     const long long most = std::max(static_cast<long long>(B) * (gamma + 1), B * 16ll);
     int ctas = 1;
     while (ctas < 8 && most > static_cast<long long>(ctas) * threads) ctas *= 2;
-    return launch_overlapped(kern, dim3(ctas), threads, smem, ctas, stream, prm);
+    const int cluster = g_barrier_extra.load() ? 1 : ctas;       // test hook: none
+    return launch_overlapped(kern, dim3(ctas), threads, smem, cluster, stream, prm);
 }
 
 int dspark_qk_norm_rope_store(const void *qkv, int64_t qkv_stride, const void *q_weight,

@@ -106,6 +106,13 @@ __global__ void __launch_bounds__(kThreads) verify_layout_kernel(const Params p)
     const int cta = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
     launch_dependents();
     wait_for_prior_kernels();
+    // the state is updated in place, and the cluster barriers are all that keeps one CTA's update
+    // from another's reads: a grid that is not one cluster (a tool re-issuing the launch without
+    // it, say) stops here, before it touches memory
+    if (cluster_nctarank() != gridDim.x || blockDim.x != kThreads) {
+        if (tid == 0) record_error(DSPARK_BAD_LAUNCH);
+        return;
+    }
     const int room = static_cast<int>(
         min(static_cast<long long>(p.max_pages) * p.ps, static_cast<long long>(INT32_MAX)));
 

@@ -1,0 +1,48 @@
+"""The verification pass at the ends of its range: references that rise in every tile, values that
+are not finite, scores and contexts of extreme size, launches in a shape that cannot run."""
+import numpy as np
+import pytest
+
+from test_gpu_verify_pass import (check_attention, ds, host, i32, make_attention,  # noqa: F401
+                                  reference_attention, torch_nan_to, with_workspace)
+
+pytestmark = pytest.mark.gpu
+
+
+def slots_of(s, b, count):
+    """(page, offset) of request b's first `count` tokens."""
+    import torch
+    ps = s["k_cache"].shape[2]
+    j = torch.arange(count, device="cuda")
+    return s["pages"][b].long()[j // ps], j % ps
+
+
+def set_keys(s, b, keys):
+    """The first len(keys) keys of request b, the same for every key head: [n, D]."""
+    page, off = slots_of(s, b, len(keys))
+    s["k_cache"][page, :, off] = keys[:, None].to(s["k_cache"].dtype).expand(
+        -1, s["k_cache"].shape[1], -1)
+
+
+@pytest.mark.parametrize("B, gamma", [(64, 16), (600, 4)])
+def test_layout_without_its_cluster(ds, B, gamma):  # noqa: F811
+    """A grid of several CTAs whose cluster is missing: reported, and nothing is touched."""
+    from test_gpu_verify_pass import STATE, check_layout, make_layout, run_layout
+    import verify_pass_ref as ref
+    s = make_layout(B, gamma, 16, 500, B, spare=2 * B)
+    d = {k: i32(s[k]) for k in STATE}
+    for k, n in (("row_start", B + 1), *((k, B * (gamma + 1)) for k in ("position", "slot", "token"))):
+        d[k] = i32(np.full(n, -7))
+    before = {k: t.clone() for k, t in d.items()}
+    ds.debug_barrier_extra(1)
+    try:
+        run_layout(ds, s, gamma, 16, out=d)
+        assert ds.get_error() == 8
+    finally:
+        ds.debug_barrier_extra(0)
+    for k, t in before.items():
+        assert bool((d[k] == t).all()), k
+    run_layout(ds, s, gamma, 16, out=d)
+    assert ds.get_error() == 0
+    check_layout(d, ref.layout(*(s[k] for k in ("L", "context", "held", "pages", "free_pages",
+                                                "free_count")), 16, s["anchor"], s["x"]))
