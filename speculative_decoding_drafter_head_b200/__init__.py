@@ -280,7 +280,7 @@ def calls(build_if_missing: bool = True):
         lib = load(build_if_missing)
         if build_if_missing and _build.calls_stale():
             _build.build_calls()
-        loader = importlib.machinery.ExtensionFileLoader("_dspark_calls", _build.CALLS)
+        loader = importlib.machinery.ExtensionFileLoader("_dspark_calls", _build.calls_path())
         mod = importlib.util.module_from_spec(
             importlib.util.spec_from_loader("_dspark_calls", loader))
         loader.exec_module(mod)

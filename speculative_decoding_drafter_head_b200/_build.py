@@ -11,7 +11,6 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libdspark.so")
-CALLS = os.path.join(PKG, "_dspark_calls.so")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
@@ -42,6 +41,17 @@ def _older(path, sources) -> bool:
     return any(os.path.getmtime(s) > t for s in sources)
 
 
+def calls_path() -> str:
+    """Where the extension module for this torch, its C++ ABI and this interpreter stands: it reads
+    tensors through their inline accessors, so a file built for another must not be loaded."""
+    import sysconfig
+
+    import torch
+    return os.path.join(PKG, f"_dspark_calls.torch{torch.__version__}"
+                             f"-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+                             f"{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def _calls_sources():
     return [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "dspark.h")]
 
@@ -51,18 +61,19 @@ def stale() -> bool:
 
 
 def calls_stale() -> bool:
-    return _older(CALLS, _calls_sources())
+    return _older(calls_path(), _calls_sources())
 
 
 def build_calls(force: bool = False, verbose: bool = False) -> str:
     """Compile csrc/binding.cpp against this interpreter and its torch."""
+    path = calls_path()
     if not force and not calls_stale():
-        return CALLS
+        return path
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension
-    tmp = CALLS + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     include = [*cpp_extension.include_paths(), os.path.join(cuda, "include"),
@@ -74,8 +85,8 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd))
     subprocess.check_call(cmd)
-    os.replace(tmp, CALLS)
-    return CALLS
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
