@@ -407,7 +407,8 @@ int dspark_qk_norm_rope_store(const void *qkv, int64_t qkv_stride, const void *q
  *   workspace, workspace_bytes >= dspark_verify_attention_workspace_bytes(Hq, Hkv, D);
  *   256-byte aligned, no initialisation needed.  Calls that can overlap need one each.
  * A page id out of range records DSPARK_INVALID_PAGE and is read as page 0; lengths beyond
- * the block table record DSPARK_INVALID_TOKEN and are clamped.
+ * the block table, and a context below zero with rows, record DSPARK_INVALID_TOKEN and are
+ * clamped.
  * Supported: D 64 or 128; Hq a multiple of Hkv, Hq / Hkv <= 112; page_size 16, 32, 64 or
  * 128; 1 <= B <= 4096; num_pages Hkv page_size < 2^31, B max_pages < 2^31; arrays 16-byte
  * aligned; scale finite.

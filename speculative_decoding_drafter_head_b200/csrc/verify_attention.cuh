@@ -173,7 +173,7 @@ __device__ __forceinline__ void load_request(const Params &p, int b, int &ctx, i
     rows = min(max(s1, start), p.row_capacity) - start;
     const int room = static_cast<int>(
         min(static_cast<long long>(p.max_pages) * p.ps, static_cast<long long>(INT32_MAX)));
-    bad = s0 != start || s1 != start + rows;
+    bad = s0 != start || s1 != start + rows || (rows > 0 && c < 0);
     ctx = max(c, 0);
     if (rows > 0 && (rows > room || ctx > room - rows)) {
         bad = true;

@@ -24,6 +24,21 @@ def set_keys(s, b, keys):
         -1, s["k_cache"].shape[1], -1)
 
 
+def test_negative_context_with_rows(ds):  # noqa: F811
+    """A length out of range is recorded and clamped, a context below zero as well."""
+    s, start = make_attention([0, 40], [2, 1], 4, 2, 64, 16, 6)
+    with_workspace(ds, s)
+    s["context"][0] = -5
+    ds.verify_attention(**s)
+    assert ds.get_error() == 7
+    s["context"][0] = 0
+    check_attention(s, int(start[-1]), 64 ** -0.5)
+    # without rows any context will do
+    s["context"][0], s["row_start"] = -5, i32([0, 0, 1])
+    ds.verify_attention(**s)
+    assert ds.get_error() == 0
+
+
 @pytest.mark.parametrize("B, gamma", [(64, 16), (600, 4)])
 def test_layout_without_its_cluster(ds, B, gamma):  # noqa: F811
     """A grid of several CTAs whose cluster is missing: reported, and nothing is touched."""
