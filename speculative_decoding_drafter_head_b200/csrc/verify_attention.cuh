@@ -1133,7 +1133,7 @@ __global__ void __launch_bounds__(kJoinThreads) verify_join_kernel(const Params 
 #pragma unroll
         for (int i = 0; i < kJoinAhead; ++i)
             if (i < parts) fetch(i, v[i]);
-        // M over all parts; a part without l saw no key
+        // M over all parts; a part without l saw no key, or none of a finite score
         float2 ml = make_float2(0.0f, 0.0f);
         if (lane < parts) ml = p.part_ml[part(lane)];
         float m = ml.y != 0.0f ? ml.x : -INFINITY;
@@ -1149,13 +1149,15 @@ __global__ void __launch_bounds__(kJoinThreads) verify_join_kernel(const Params 
                 ml = make_float2(0.0f, 0.0f);
                 if (i0 + lane < parts) ml = p.part_ml[part(i0 + lane)];
             }
+            // a weight of nothing still multiplies: zero times a value that is not finite is NaN,
+            // as it is within a part (a row that saw no key of a part left zeros there)
             const float f = ml.y != 0.0f ? exp2_approx(ml.x - m) : 0.0f;
             l += ml.y * f;
             for (int g = i0; g < min(i0 + 32, parts); g += kJoinAhead) {
 #pragma unroll
                 for (int e = 0; e < kJoinAhead; ++e) {
                     const float w = __shfl_sync(0xFFFFFFFFu, f, g + e - i0);
-                    if (g + e < parts && w != 0.0f)
+                    if (g + e < parts)
 #pragma unroll
                         for (int j = 0; j < kPer; ++j) acc[j] = fmaf(v[e][j], w, acc[j]);
                     if (g + e + kJoinAhead < parts) fetch(g + e + kJoinAhead, v[e]);

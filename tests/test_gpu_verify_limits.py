@@ -24,6 +24,35 @@ def set_keys(s, b, keys):
         -1, s["k_cache"].shape[1], -1)
 
 
+@pytest.mark.parametrize("low", [0.0, float("-inf")])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_seen_value_in_a_part_of_no_weight(ds, value, D, low):  # noqa: F811
+    """A value that is not finite reaches the rows that see it, whatever its key's weight rounds
+    to: zero times it is NaN.  So also where a part of a cut unit has no weight beside the others,
+    or none at all."""
+    import torch
+    s, start = make_attention([2000], [2], 2, 1, D, 16, 8)
+    k = torch.zeros(2002, D, device="cuda")
+    k[:, 0] = low
+    k[1000:, 0] = 300.0
+    set_keys(s, 0, k)
+    s["q"].zero_()
+    s["q"][:, :, 0] = 1.0
+    page, off = slots_of(s, 0, 11)
+    s["v_cache"][page[10], 0, off[10], 5] = value
+    with_workspace(ds, s)
+    ds.verify_attention(**s, scale=1.0)
+    assert ds.get_error() == 0
+    got = s["out"].double()
+    assert not bool(got[:, :, 5].isfinite().any())
+    s["v_cache"] = torch_nan_to(s["v_cache"])
+    out, mag = reference_attention(s, 1.0)
+    tol = 2.0 ** -8 * out.abs() + (2.0 ** -7 + 2.0 ** -9) * mag
+    ok = (got - out).abs() <= tol
+    assert bool(ok[:, :, :5].all()) and bool(ok[:, :, 6:].all())
+
+
 def test_negative_context_with_rows(ds):  # noqa: F811
     """A length out of range is recorded and clamped, a context below zero as well."""
     s, start = make_attention([0, 40], [2, 1], 4, 2, 64, 16, 6)
