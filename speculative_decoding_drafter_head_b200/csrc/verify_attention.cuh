@@ -835,8 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (c0 + 16 < s.rows) tmem_ld_32x32b_x16(lane_base + C::kColO + ob * kN + c0 + 16, o);
                 if (odd && has_d) {               // values that are not finite, to who sees them
-                    for (int j = max(s.kt * kTileKeys, s.hidden);
-                         j < min(s.kt_end * kTileKeys, s.keys); ++j) {
+                    const int end = s.ends ? s.keys : s.kt_end * kTileKeys;
+                    for (int j = max(s.kt * kTileKeys, s.hidden); j < end; ++j) {
                         int page = p.pages[static_cast<size_t>(s.b) * p.max_pages + j / p.ps];
                         if (page < 0 || page >= p.num_pages) page = 0;
                         const uint32_t x =
@@ -928,7 +928,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int from = 0;
                 if (key >= cur.keys) from = kMaxRows;
                 else if (key >= cur.hidden) from = (key - cur.hidden + 1) * p.group;
-                const bool masked = (kt + 1) * kTileKeys > cur.hidden;
+                // (a tile's end may be past 32 bits)
+                const bool masked = kt * kTileKeys > cur.hidden - kTileKeys;
                 const bool first = kt == cur.kt;
                 const uint32_t before = p_full + 8 * (wg ^ 1), before_phase = ((i - 1) >> 1) & 1u;
                 await(tile_bar(s_full, i), tile_phase(i));

@@ -68,6 +68,27 @@ def test_negative_context_with_rows(ds):  # noqa: F811
     assert ds.get_error() == 0
 
 
+def test_longest_context(ds):  # noqa: F811
+    """A context of 2^31 - 2 tokens (its pages are the same few over and over): the last tile's
+    end is past 32 bits, and the key behind the last one stays hidden."""
+    import torch
+    D, ps = 64, 16
+    pages = torch.zeros(1, (1 << 31) // ps, dtype=torch.int32, device="cuda")
+    pages[0, -1] = 1
+    k, v = (torch.zeros(2, 1, ps, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k[1, 0, 14, 0], k[1, 0, 15, 0] = 60.0, 120.0
+    v[1, 0, 14], v[1, 0, 15] = 3.0, 100.0
+    q = torch.zeros(1, 1, D, dtype=torch.bfloat16, device="cuda")
+    q[0, 0, 0] = 1.0
+    s = dict(q=q, k_cache=k, v_cache=v, pages=pages, context=i32([2 ** 31 - 2]),
+             row_start=i32([0, 1]), out=torch.full_like(q, 9.0))
+    with_workspace(ds, s)
+    ds.verify_attention(**s, scale=1.0)
+    assert ds.get_error() == 0
+    # e^60 beside 2^31 keys of weight 1: three, to 2^-55
+    assert bool((s["out"] == 3.0).all())
+
+
 @pytest.mark.parametrize("B, gamma", [(64, 16), (600, 4)])
 def test_layout_without_its_cluster(ds, B, gamma):  # noqa: F811
     """A grid of several CTAs whose cluster is missing: reported, and nothing is touched."""
