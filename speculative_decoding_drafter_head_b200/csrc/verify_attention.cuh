@@ -20,7 +20,10 @@
 // new maximum and O and l are scaled (one vote a tile, folded into the barrier that a tile
 // needs anyway).  bf16 weights keep their 8 bits at any magnitude, and O and l are fp32, so
 // a stale m costs no accuracy.  A row without a finite score so far has an m below any, so that
-// its first one raises it.  The weights are rounded to bf16 (by 2^-8 of each at most, as the
+// its first one raises it.  A weight's exponent is one fma, score scale - m; but m is a rounded
+// product itself, by up to 16 and more from |m| = 2^28 on, so there the product is rounded as m
+// was and the maximum's exponent is zero again (a step's other rows, which lose nothing that counts
+// by it, go the same way).  The weights are rounded to bf16 (by 2^-8 of each at most, as the
 // output itself), which is what the tensor core's second product asks for.
 //
 // Masks: key j is seen by the rows from (j - context) g on, so a thread compares the row's
@@ -50,6 +53,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <cfloat>
+
 #include "common.cuh"
 #include "ptx.cuh"
 #include "verify_plan.h"
@@ -70,7 +75,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWaitHintNs = 20000;
 constexpr int kLooks = 4096;                      // at two barriers in turn, before a wait for one
 constexpr float kRaise = 24.0f;                   // log2 of the weight at which m rises
-constexpr float kUnset = -1e30f;                  // m of a row that has met no finite score yet
+constexpr float kUnset = -FLT_MAX;                // m of a row that has met no finite score yet
+// From this size of m on, half a step of an fp32 score is more than a weight's range.
+constexpr float kFar = 0x1p28f;
 constexpr int kOnesBytes = 1152;                  // 8 x 2 core matrices of 128 B, one apart
 constexpr int kJoinThreads = 256;
 constexpr int kJoinAhead = 8;                     // parts whose O a row has in flight
@@ -154,6 +161,7 @@ struct Ctl {
     int abort;
     int epoch;                                    // times that a reference m rose
     int odd[8];                                   // a cleared value, by segment as for m
+    int far[8];                                   // an m of kFar or more, likewise
     int seg_n[2], seg_tiles[2];                   // the segment of a Q buffer; no tiles: the end
 };
 
@@ -461,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_fence_init();
         ctl.abort = 0;
         ctl.epoch = 0;
-        for (int i = 0; i < 8; ++i) ctl.odd[i] = 0;
+        for (int i = 0; i < 8; ++i) ctl.odd[i] = ctl.far[i] = 0;
     }
     if (warp == kWarpMma) {
         tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
@@ -872,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             group_sync(wg);                       // red is free again
-            if (at == 0) ctl.odd[seg % C::kMBufs] = 0;
+            if (at == 0) ctl.odd[seg % C::kMBufs] = ctl.far[seg % C::kMBufs] = 0;
             tc_fence_before();
             mbar_arrive(o_empty + 8 * ob);
         };
@@ -955,6 +963,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         group_sync(wg);
                         if (at < n) {
                             const float m = share ? red[((at >> 4) & 3) * kN + at] : max_of(at);
+                            if (fabsf(m) >= kFar && m != -INFINITY)
+                                *reinterpret_cast<volatile int *>(&ctl.far[seg % C::kMBufs]) = 1;
                             if (task == 1) {
                                 m_row[at] = m == -INFINITY ? kUnset : m;
                             } else {
@@ -993,6 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // weights to shared memory; the largest log2 of one
                     const int epoch = *reinterpret_cast<volatile int *>(&ctl.epoch);
+                    const bool far = *reinterpret_cast<volatile int *>(&ctl.far[seg % C::kMBufs]);
                     float top = -INFINITY;
 #pragma unroll 1
                     for (int c = 0; c < n; c += 16) {
@@ -1004,12 +1015,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                             m[q] = *reinterpret_cast<const float4 *>(m_row + c + 4 * q);
                         tmem_wait_ld16(r);
                         float t[16];
+                        if (!far) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            scaled2(t[4 * q], t[4 * q + 1], r[4 * q], r[4 * q + 1], sl, m[q].x,
-                                    m[q].y);
-                            scaled2(t[4 * q + 2], t[4 * q + 3], r[4 * q + 2], r[4 * q + 3], sl,
-                                    m[q].z, m[q].w);
+                            for (int q = 0; q < 4; ++q) {
+                                scaled2(t[4 * q], t[4 * q + 1], r[4 * q], r[4 * q + 1], sl, m[q].x,
+                                        m[q].y);
+                                scaled2(t[4 * q + 2], t[4 * q + 3], r[4 * q + 2], r[4 * q + 3], sl,
+                                        m[q].z, m[q].w);
+                            }
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const float f[4] = {m[q].x, m[q].y, m[q].z, m[q].w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    t[4 * q + e] = __fsub_rn(
+                                        __fmul_rn(__uint_as_float(r[4 * q + e]), sl), f[e]);
+                            }
                         }
                         if (masked) {
 #pragma unroll

@@ -53,6 +53,54 @@ def test_seen_value_in_a_part_of_no_weight(ds, value, D, low):  # noqa: F811
     assert bool(ok[:, :, :5].all()) and bool(ok[:, :, 6:].all())
 
 
+@pytest.mark.parametrize("others", [0, 230])
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 14, 2.0 ** 17, 2.0 ** 40, -2.0 ** 14, -2.0 ** 40])
+@pytest.mark.parametrize("D, tokens", [(64, 3), (128, 20)])
+def test_scores_of_any_size(ds, D, tokens, size, others):  # noqa: F811
+    """Scores far beyond 2^24, where a score's own rounding is more than a weight's range: the
+    largest take all, in equal shares."""
+    import torch
+    ctx = [700, 40] + [50] * others
+    s, start = make_attention(ctx, [tokens] * len(ctx), 8, 2, D, 16, 31)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for b in range(len(ctx)):
+        n = ctx[b] + tokens
+        k = torch.zeros(n, D, device="cuda")
+        k[:, 0] = abs(size) * (1 + torch.randint(0, 40, (n,), generator=g, device="cuda") / 64)
+        set_keys(s, b, k)
+    s["q"].zero_()
+    s["q"][:, :, 0] = size * (1 + torch.arange(8, device="cuda") / 8)
+    with_workspace(ds, s)
+    ds.verify_attention(**s, scale=1.0)
+    assert ds.get_error() == 0
+    # scores are single products of two bf16, exact, and differ by 2^-7 of their size at least:
+    # 2^17 in natural logarithms from 2^24 on, so the weights are 1 or 0 in any arithmetic
+    check_attention(s, int(start[-1]), 1.0)
+
+
+def test_scores_below_any_reference(ds):  # noqa: F811
+    """Finite scores of -1e36 behind keys whose scores are -inf."""
+    import torch
+    D, others = 128, 230
+    ctx = [256, 200] + [40] * others
+    s, start = make_attention(ctx, [1] * len(ctx), 4, 2, D, 16, 32)
+    for b in range(2):
+        n = ctx[b] + 1
+        k = torch.zeros(n, D, device="cuda")
+        k[:, 0] = 2.0 ** 60
+        k[:160, 0] = float("inf")
+        set_keys(s, b, k)
+    for b in range(2, len(ctx)):
+        set_keys(s, b, torch.full((41, D), 2.0 ** 60, device="cuda"))
+    s["q"].zero_()
+    s["q"][:, :, 0] = -2.0 ** 60
+    with_workspace(ds, s)
+    ds.verify_attention(**s, scale=1.0)
+    assert ds.get_error() == 0
+    # every weight that is not nothing is the same
+    check_attention(s, int(start[-1]), 1.0)
+
+
 def test_negative_context_with_rows(ds):  # noqa: F811
     """A length out of range is recorded and clamped, a context below zero as well."""
     s, start = make_attention([0, 40], [2, 1], 4, 2, 64, 16, 6)
