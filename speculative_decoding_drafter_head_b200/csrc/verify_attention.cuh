@@ -425,6 +425,63 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w)
     return w;
 }
 
+// The weights of a thread's key against a tile's n rows, from S in tensor memory to P in shared
+// memory; returns the largest log2 of one.  Rows below `from` do not see the key.
+template <bool kIsFar>
+__device__ __forceinline__ float make_weights(uint32_t col, int n, const float *m_row, float sl,
+                                              bool masked, int from, uint32_t prow)
+{
+    const int at = threadIdx.x & 127;
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < n; c += 16) {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(col + c, r);
+        float4 m[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m[q] = *reinterpret_cast<const float4 *>(m_row + c + 4 * q);
+        tmem_wait_ld16(r);
+        float t[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if constexpr (!kIsFar) {
+                scaled2(t[4 * q], t[4 * q + 1], r[4 * q], r[4 * q + 1], sl, m[q].x, m[q].y);
+                scaled2(t[4 * q + 2], t[4 * q + 3], r[4 * q + 2], r[4 * q + 3], sl, m[q].z, m[q].w);
+            } else {
+                const float f[4] = {m[q].x, m[q].y, m[q].z, m[q].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    t[4 * q + e] =
+                        __fsub_rn(__fmul_rn(__uint_as_float(r[4 * q + e]), sl), f[e]);
+            }
+        }
+        if (masked) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (c + j < from) t[j] = -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) top = max3(top, t[j], t[j + 1]);
+        uint32_t word[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            word[j] = pack2_bf16(exp2_approx(t[2 * j]), exp2_approx(t[2 * j + 1]));
+        const uint32_t to = prow + (c >> 6) * (kTileKeys * 128);
+        const int u = (c >> 3) & 7;
+        sts128(to + ((u ^ (at & 7)) << 4), word[0], word[1], word[2], word[3]);
+        sts128(to + (((u + 1) ^ (at & 7)) << 4), word[4], word[5], word[6], word[7]);
+    }
+    return top;
+}
+
+// The same where an m is kFar or more: a call, to keep the loop that makes it short (the choice
+// inside the loop made tiles of 112 rows 4% slower).
+__device__ __noinline__ float make_far_weights(uint32_t col, int n, const float *m_row, float sl,
+                                               int from, uint32_t prow)
+{
+    return make_weights<true>(col, n, m_row, sl, true, from, prow);
+}
+
 template <int D, int kN>
 __global__ void __launch_bounds__(kThreads, 1)
     verify_attention_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -451,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t q_full = smem_u32(ctl.q_full);
     const uint32_t q_empty = smem_u32(ctl.q_empty);
     const uint32_t o_empty = smem_u32(ctl.o_empty), drain = smem_u32(&ctl.drain);
+    if (tid >= 32 && tid < 40) ctl.odd[tid - 32] = ctl.far[tid - 32] = 0;
     if (tid == 0) {
         for (uint32_t i = 0; i < kTileBars; ++i) {
             mbar_init(k_full + 8 * i, 1);
@@ -469,7 +527,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_fence_init();
         ctl.abort = 0;
         ctl.epoch = 0;
-        for (int i = 0; i < 8; ++i) ctl.odd[i] = ctl.far[i] = 0;
     }
     if (warp == kWarpMma) {
         tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
@@ -1003,52 +1060,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // weights to shared memory; the largest log2 of one
                     const int epoch = *reinterpret_cast<volatile int *>(&ctl.epoch);
-                    const bool far = *reinterpret_cast<volatile int *>(&ctl.far[seg % C::kMBufs]);
-                    float top = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < n; c += 16) {
-                        uint32_t r[16];
-                        tmem_ld_32x32b_x16(col + c, r);
-                        float4 m[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            m[q] = *reinterpret_cast<const float4 *>(m_row + c + 4 * q);
-                        tmem_wait_ld16(r);
-                        float t[16];
-                        if (!far) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                scaled2(t[4 * q], t[4 * q + 1], r[4 * q], r[4 * q + 1], sl, m[q].x,
-                                        m[q].y);
-                                scaled2(t[4 * q + 2], t[4 * q + 3], r[4 * q + 2], r[4 * q + 3], sl,
-                                        m[q].z, m[q].w);
-                            }
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const float f[4] = {m[q].x, m[q].y, m[q].z, m[q].w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    t[4 * q + e] = __fsub_rn(
-                                        __fmul_rn(__uint_as_float(r[4 * q + e]), sl), f[e]);
-                            }
-                        }
-                        if (masked) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (c + j < from) t[j] = -INFINITY;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) top = max3(top, t[j], t[j + 1]);
-                        uint32_t word[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            word[j] = pack2_bf16(exp2_approx(t[2 * j]), exp2_approx(t[2 * j + 1]));
-                        const uint32_t to = prow + (c >> 6) * (kTileKeys * 128);
-                        const int u = (c >> 3) & 7;
-                        sts128(to + ((u ^ (at & 7)) << 4), word[0], word[1], word[2], word[3]);
-                        sts128(to + (((u + 1) ^ (at & 7)) << 4), word[4], word[5], word[6], word[7]);
-                    }
+                    // (the whole warp takes the same way; the other group may be raising m meanwhile,
+                    // and then these weights are stale)
+                    const bool far = __any_sync(
+                        0xFFFFFFFFu, *reinterpret_cast<volatile int *>(&ctl.far[seg % C::kMBufs]));
+                    const float top =
+                        far ? make_far_weights(col, n, m_row, sl, from, prow)
+                            : make_weights<false>(col, n, m_row, sl, masked, from, prow);
                     if (masked && tries == 0) {
                         // values behind the last key, and those that are not finite: the last
                         // thing, since the values come after the keys
