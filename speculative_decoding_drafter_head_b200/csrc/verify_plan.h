@@ -41,29 +41,31 @@ DSPARK_HD long long quotient(long long a, long long b)
     return a / b;
 }
 
-// sum over i = 0 .. n - 1 of floor((a i + b) / 2^7), a, b >= 0, by Euclid's steps
+// Key tiles of query tiles 0 .. n - 1, all of them full: the sum of floor(e / 128) over the ends
+// e = b, b + a, ..., b + (n - 1) a (a, b >= 0).
+//
+// An end's place in its key tile, e mod 128, comes back after 128 query tiles, in which the ends
+// have moved by a whole key tiles.  So with n = 128 u + v the u whole rounds follow from the first:
+// its places run through the classes r, r + g, r + 2 g, ... below 128 (g = gcd(a, 128), a power
+// of two; r = b mod g) g times each, so they add up to 64 (128 - g + 2 r), and what is left of the
+// ends' sum is 128 times their tiles'.  The v ends behind the last round are added up one by one:
+// 127 at most, of an addition and a shift each, where divisions by the step take longer.
 // (a call: only requests of three query tiles or more come here, and inlined where it is used it
 // is most of what a CTA fetches as instructions before its first copy)
-DSPARK_HD_CALL long long floor_sum(long long n, long long a, long long b)
+DSPARK_HD_CALL long long tiles_of(long long n, int a, long long b)
 {
-    long long m = kTileKeys, sum = 0;
-    while (true) {
-        if (a >= m) {
-            sum += n * (n - 1) / 2 * (a / m);
-            a %= m;
-        }
-        if (b >= m) {
-            sum += n * (b / m);
-            b %= m;
-        }
-        const long long top = a * n + b;
-        if (top < m) return sum;
-        n = top / m;
-        b = top % m;
-        const long long t = m;
-        m = a;
-        a = t;
-    }
+    static_assert(kTileKeys == 128, "the shifts below");
+    const long long u = n >> 7;
+    const int v = static_cast<int>(n & 127);
+    const int g = (a | 128) & -(a | 128);             // gcd(a, 128)
+    const int r = static_cast<int>(b & (g - 1));
+    // tiles of the first round: (sum of its ends - sum of their places) / 128
+    const long long round = b + ((127ll * a - (128 - g + 2 * r)) >> 1);
+    long long sum = u * round + 64 * a * u * (u - 1);
+    const long long from = b + 128 * a * u;           // the first end behind the rounds
+    int e = static_cast<int>(from & 127), part = 0;
+    for (int i = 0; i < v; ++i, e += a) part += e >> 7;
+    return sum + v * (from >> 7) + part;
 }
 
 struct Request {
@@ -95,7 +97,7 @@ struct Request {
         const int full = qt < query_tiles() ? qt : query_tiles() - 1;
         long long sum = 0;
         if (full > 0)
-            sum = floor_sum(full, tokens, static_cast<long long>(ctx) + tokens + kTileKeys - 1) *
+            sum = tiles_of(full, tokens, static_cast<long long>(ctx) + tokens + kTileKeys - 1) *
                   tile_places(0);
         if (full < qt) sum += static_cast<long long>(key_tiles(full)) * tile_places(full);
         return sum + static_cast<long long>(qt) * kUnitPlaces;
