@@ -24,6 +24,82 @@ def set_keys(s, b, keys):
         -1, s["k_cache"].shape[1], -1)
 
 
+# Query tiles of up to 64 rows, and of up to 112 where the row capacity asks for more; 3 and 17
+# tokens leave the last 16 columns in part empty, 16 and 28 fill the tile.
+@pytest.mark.parametrize("tokens", [3, 16, 17, 28])
+@pytest.mark.parametrize("D", [64, 128])
+def test_reference_rises_in_every_tile(ds, D, tokens):  # noqa: F811
+    """One row's scores jump by 2^29 in weight from tile to tile, so that every tile raises the
+    references of all rows; the others' rise by factors of 0.13 to 0.8, so that O and l of the
+    tiles before, scaled, are much of the result.  Some twelve tiles to a segment: both softmax
+    groups raise, and find weights that the other has made stale."""
+    import torch
+    rng = np.random.default_rng(D + tokens)
+    B, Hq, Hkv = 37, 16, 4
+    ctx = 1400 + 5 * rng.integers(0, 60, B)
+    s, start = make_attention(ctx, [tokens] * B, Hq, Hkv, D, 16, D + tokens)
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    for b in range(B):
+        n = int(ctx[b]) + tokens
+        k = torch.zeros(n, D, device="cuda")
+        k[:, 0] = torch.arange(n, device="cuda") // 128
+        k[:, 1] = torch.rand(n, generator=g, device="cuda") * 2 - 1
+        set_keys(s, b, k)
+    q = torch.zeros(s["q"].shape, device="cuda")
+    r = torch.arange(q.shape[0] * Hq, device="cuda").reshape(-1, Hq)
+    q[:, :, 0] = 0.25 + 0.25 * (r % 8)
+    q[:, :, 1] = torch.rand(r.shape, generator=g, device="cuda") * 2 - 1
+    # the row that jumps: one of each request's, in every key head
+    at = torch.from_numpy(start[:-1] + rng.integers(0, tokens, B)).cuda()
+    q[at, 1::4, 0] = 20.0
+    s["q"] = q.bfloat16()
+    with_workspace(ds, s)
+    ds.verify_attention(**s, scale=1.0)
+    assert ds.get_error() == 0
+    # scores of two exact products, below 20 x 14: fp32 is off by 2^-15 in one of them, and the
+    # scaling of O and l by 2^-22 of a factor a tile, far within check_attention's 2^-9
+    check_attention(s, int(start[-1]), 1.0)
+    out, _ = reference_attention(s, 1.0)
+    last = out.clone()                                 # without the first ten tiles
+    for b in range(B):
+        page, off = slots_of(s, b, 1280)
+        s["k_cache"][page, :, off, 0] = -200.0
+    last, _ = reference_attention(s, 1.0)
+    slow = s["q"][:, :, 0].float() == 0.25
+    assert float((out - last).abs()[slow].mean()) > 0.02     # the tiles before do count
+
+
+@pytest.mark.parametrize("others", [0, 230])               # units in parts, and whole ones
+@pytest.mark.parametrize("D, tokens", [(64, 8), (64, 20), (128, 8), (128, 20)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_hidden_values_everywhere(ds, value, D, tokens, others):  # noqa: F811
+    """A later row's key or value that is not finite reaches the rows that see it, no other: both
+    head sizes, both query tiles, with and without a join."""
+    rng = np.random.default_rng(5)
+    ctx = [250, 100] + list(rng.integers(0, 300, others))
+    s, start = make_attention(ctx, [tokens] * len(ctx), 8, 2, D, 16, 4)
+    pages = host(s["pages"])
+    for cache, b, pos in (("v_cache", 0, 254), ("k_cache", 1, 103), ("v_cache", 1, 106)):
+        s[cache][int(pages[b, pos // 16]), 1, pos % 16, 17] = value
+    with_workspace(ds, s)
+    ds.verify_attention(**s)
+    assert ds.get_error() == 0
+    got = s["out"].double()
+    clean = dict(s)
+    clean["k_cache"], clean["v_cache"] = (torch_nan_to(s[k]) for k in ("k_cache", "v_cache"))
+    out, mag = reference_attention(clean, D ** -0.5)
+    tol = 2.0 ** -8 * out.abs() + (2.0 ** -7 + 2.0 ** -9) * mag
+    ok = (got - out).abs() <= tol
+    assert bool(ok[:, :4].all())                            # the other key head
+    assert bool(ok[:4].all())                               # request 0, rows before the value
+    rest = ok[4:tokens, 4:]
+    assert bool(rest[..., :17].all()) and bool(rest[..., 18:].all())
+    bad = got[4:tokens, 4:, 17]
+    assert bool(bad.isnan().all()) if value != value else bool((bad == value).all())
+    assert bool(ok[tokens:tokens + 3].all())                # request 1, rows before the key
+    assert bool(ok[2 * tokens:].all())                      # the other requests
+
+
 @pytest.mark.parametrize("low", [0.0, float("-inf")])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
