@@ -398,9 +398,11 @@ int dspark_qk_norm_rope_store(const void *qkv, int64_t qkv_stride, const void *q
  * 0 .. context[b] + i (its own among them: store them first), g = Hq / Hkv query heads to a
  * key head:
  *   out[r, h] = sum_j p_j v[j, h / g],  p = softmax_j(scale q[r, h] . k[j, h / g])
- * fp32 scores, sums and accumulators.  Keys that a row does not see take no part, whatever
- * their slots hold, NaN and infinities included; a value that is not finite reaches every row
- * that sees it, however small its key's weight.
+ * fp32 scores, sums and accumulators; each weight p is rounded to bf16 for its product with the
+ * values and for the sum that it is divided by, which the tensor cores' operand asks for, so the
+ * output is off by up to 2^-8 of sum_j p_j |v_j - out| beside its own rounding.  Keys that a row
+ * does not see take no part, whatever their slots hold, NaN and infinities included; a value that
+ * is not finite reaches every row that sees it, however small its key's weight.
  *   q, out [row_capacity, Hq, D] bf16, not overlapping; rows of out behind the last request's
  *   are left as they are
  *   pages [B, max_pages], context [B], row_start [B + 1] int32 as dspark_verify_layout leaves

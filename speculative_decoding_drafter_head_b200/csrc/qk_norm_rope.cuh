@@ -14,8 +14,8 @@
 //
 // What bounds it: HBM, every channel read and written once, which takes some 70 KB on their way
 // to each SM: more than registers hold beside the arithmetic, so channels go to shared memory
-// first (13000 rows of 48 heads of 128: 61 us with two units of 512 bytes ahead in registers,
-// 54 with six in shared memory, 56 with four, 57 with ten).  8 channels a lane leave room for
+// first (13000 rows of 48 heads of 128: 62.4 us with two units of 512 bytes ahead in registers,
+// 55.6 with six in shared memory, 56.3 with four, 57.5 with ten).  8 channels a lane leave room for
 // some 100 instructions.  So a lane holds whole rotation pairs (4 channels from each half,
 // or 8 neighbours when interleaved) and needs no exchange for them, and the weights times
 // cosines and sines of its channels stay in registers for all heads of a row:

@@ -24,7 +24,8 @@
 // product itself, by up to 16 and more from |m| = 2^28 on, so there the product is rounded as m
 // was and the maximum's exponent is zero again (a step's other rows, which lose nothing that counts
 // by it, go the same way).  The weights are rounded to bf16 (by 2^-8 of each at most, as the
-// output itself), which is what the tensor core's second product asks for.
+// output itself), which is what the tensor core's second product asks for: against 64 bits the
+// output is off by 0.0021 to 0.0024 of its norm, where rounding it alone makes 0.0017.
 //
 // Masks: key j is seen by the rows from (j - context) g on, so a thread compares the row's
 // number with one number of its own.  Values behind the last key are cleared in shared memory
@@ -44,9 +45,9 @@
 // softmax.
 //
 // Measured (B200, device time): 64 requests, 32/8 heads of 128, 500-8000 keys, up to 17 rows
-// each 178 us, 6.2 TB/s of the 6.47 a copy reaches; 256 requests of one row, 32/4 heads 305 us,
-// 6.7 TB/s; one request of 131 thousand keys 90 us, 6.0 TB/s; one token over 700 keys 10 us, of which
-// 4 go before the first tile has come (launch, lengths, this CTA's share, page ids, the tile).
+// each 177 us, 6.2 TB/s of the 6.47 a copy reaches; 256 requests of one row, 32/4 heads 304 us,
+// 6.7 TB/s; one request of 131 thousand keys 90 us, 6.0 TB/s; one token over 700 keys 10.6 us,
+// of which 4 go before the first tile has come (launch, lengths, this CTA's share, page ids, the tile).
 // With few keys to a unit its start and end are the bound: 2 us a unit of one tile and 4 rows,
 // 2.6 of 32, 5.4 of 112 (Q in, the reference, the output), which overlap the other group's.
 #pragma once

@@ -32,7 +32,7 @@ can be captured as one CUDA graph (one graph per ring phase) and replayed.
 verification: the paged cache of every layer, its block tables and free pages, and the
 buffers of one step's ragged batch.  A step is
 
-    L = sched.lengths(t)                              # or step()'s L_out
+    L = sched.lengths(t)                              # or schedule_prefix's L_out
     vp.layout(L, anchor, x, accepted)                 # batch of this step, pages, slots
     for layer in range(layers):                       # the target's own products around it
         out = vp.attend(layer, qkv(layer), q_weight, k_weight)
