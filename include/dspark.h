@@ -414,7 +414,7 @@ int dspark_qk_norm_rope_store(const void *qkv, int64_t qkv_stride, const void *q
  * clamped.
  * Supported: D 64 or 128; Hq a multiple of Hkv, Hq / Hkv <= 112; page_size 16, 32, 64 or
  * 128; 1 <= B <= 4096; num_pages Hkv page_size < 2^31, B max_pages < 2^31; arrays 16-byte
- * aligned; scale finite.
+ * aligned; scale, and scale times log2(e), finite in fp32.
  */
 size_t dspark_verify_attention_workspace_bytes(int Hq, int Hkv, int D);
 int dspark_verify_attention(const void *q, const void *k_cache, const void *v_cache,

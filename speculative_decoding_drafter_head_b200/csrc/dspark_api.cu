@@ -844,6 +844,8 @@ int dspark_verify_attention(const void *q, const void *k_cache, const void *v_ca
         !aligned(pages, 4) || !aligned(context, 4) || !aligned(row_start, 4) ||
         !aligned(workspace, 256) || !std::isfinite(scale))
         return DSPARK_INVALID_ARG;
+    const float scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    if (!std::isfinite(scale_log2)) return DSPARK_INVALID_ARG;
     if ((D != 64 && D != 128) || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > A::kMaxRows ||
         (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) || B < 1 ||
         B > A::kMaxB || row_capacity < 1 || max_pages < 1 || num_pages < 1 ||
@@ -888,7 +890,7 @@ int dspark_verify_attention(const void *q, const void *k_cache, const void *v_ca
     prm.ps = page_size;
     prm.max_pages = max_pages;
     prm.num_pages = num_pages;
-    prm.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    prm.scale_log2 = scale_log2;
     prm.out = static_cast<uint16_t *>(out);
     prm.desc = reinterpret_cast<int4 *>(ws);
     prm.part_ml = reinterpret_cast<float2 *>(ws + lay.ml);
